@@ -66,12 +66,23 @@ typedef uint16_t gg_bf16;
 #define GG_DEV_BAD_ROW_INDEX 2
 #define GG_DEV_SIZES_MISMATCH 3
 #define GG_DEV_TIMEOUT 4
+#define GG_DEV_BAD_ADAPTER_ID 5
 
 #define GG_MAX_EXPERTS 2048
 #define GG_MAX_TOPK 64
 #define GG_ROUTE_NOALLOC_SCRATCH_BYTES (1u << 20)
 /* gg_forward_combine without a workspace (bf16 accumulation) takes topk up to this */
 #define GG_COMBINE_BF16_MAX_TOPK 16
+/* low-rank adapters: largest rank (a multiple of 8) */
+#define GG_LORA_MAX_RANK 256
+/* rotary positions: position axes a pair can take its angle from, heads of q and k together */
+#define GG_ROPE_MAX_AXES 4
+#define GG_ROPE_MAX_HEADS 65536
+
+/* element types of gg_rope */
+#define GG_DTYPE_BF16 0
+#define GG_DTYPE_F16 1
+#define GG_DTYPE_F32 2
 
 /* operations for gg_workspace_size */
 #define GG_OP_ROUTE 1            /* gg_route_hist_offsets */
@@ -387,6 +398,73 @@ int gg_ep_plan(const int32_t* m_sizes, const int32_t* recv_m, int G, int E_loc, 
  * GG_DEV_SIZES_MISMATCH; rows past the counted ones get -1. */
 int gg_ep_recv_map(const int32_t* recv_m, int G, int E_loc, int64_t R_loc, int32_t* row_map,
                    int32_t* status, void* stream);
+
+/* ------------------------------------------------------ low-rank adapters --
+ * One shared projection W with the low-rank adapters of many requests beside
+ * it: each token's row takes its own adapter a = ids[t] (-1: none).
+ *   U[t] = bf16( scale[a] * (X[t] @ A[a]^T) )            (0 without an adapter)
+ *   Y[t] = bf16( X[t] @ W^T + U[t] @ B[a]^T )            (fp32 accumulate)
+ * Rows stay in the caller's order; ids may come in runs (sequences) or mixed.
+ *  X [T, K], W [N, K], A [L, r, K], B [L, N, r], Y [T, N], U [T, r] bf16, rows
+ *  contiguous; scale [L] fp32, or NULL for 1.  r a multiple of 8, at most
+ *  GG_LORA_MAX_RANK (a smaller rank is zero-padded by the caller); N, K
+ *  multiples of 8; L <= GG_MAX_EXPERTS.  A row is computed from its own adapter
+ *  alone: infinities or NaN in one adapter or row reach no other row.
+ *  U is kept for the backward (needed by it alone).  No counterpart on the
+ *  pages.
+ *
+ * gg_lora_plan reads a batch's ids once: the adapters that occur in each 256
+ * rows, as row masks, and the rows sorted by adapter, into a buffer of
+ * gg_lora_plan_size(T, L) bytes (16-byte aligned; 0 bytes: T or L out of
+ * range).  One plan serves every projection and layer of the batch, forward and
+ * backward.  An id outside [-1, L) sets GG_DEV_BAD_ADAPTER_ID and counts as -1. */
+size_t gg_lora_plan_size(int64_t T, int L);
+int gg_lora_plan(const int32_t* ids, int64_t T, int L, void* plan, size_t plan_bytes, int32_t* status,
+                 void* stream);
+int gg_lora_forward(const gg_bf16* X, const gg_bf16* W, const gg_bf16* A, const gg_bf16* B,
+                    const float* scale, const void* plan, int64_t T, int L, int r, int64_t N,
+                    int64_t K, gg_bf16* Y, gg_bf16* U, int32_t* status, void* stream);
+
+/* Gradient of gg_lora_forward (W is frozen; gg_backward_dW gives its gradient):
+ *   V[t]  = scale[a] * (dY[t] @ B[a])                     (kept in the workspace)
+ *   dX[t] = bf16( dY[t] @ W + V[t] @ A[a] )
+ *   dA[a] = bf16( sum over tokens t of adapter a of outer(V[t], X[t]) )
+ *   dB[a] = bf16( sum over tokens t of adapter a of outer(dY[t], U[t]) )
+ *  dY [T, N], U [T, r] the forward's; dX [T, K], dA [L, r, K], dB [L, N, r] out,
+ *  each may be NULL (not computed; its operands may then be NULL too: X for dA,
+ *  U for dB, W and A for dX).  An adapter without tokens gets zeros.
+ *  workspace: gg_lora_backward_workspace_size(T, r) bytes, 16-byte aligned
+ *  (needed for dX and dA).  Deterministic (fixed reduction orders). */
+size_t gg_lora_backward_workspace_size(int64_t T, int r);
+int gg_lora_backward(const gg_bf16* dY, const gg_bf16* X, const gg_bf16* W, const gg_bf16* A,
+                     const gg_bf16* B, const float* scale, const void* plan, const gg_bf16* U,
+                     int64_t T, int L, int r, int64_t N, int64_t K, gg_bf16* dX, gg_bf16* dA,
+                     gg_bf16* dB, void* workspace, size_t workspace_bytes, int32_t* status,
+                     void* stream);
+
+/* -------------------------------------------------------- rotary positions --
+ * Rotary positions on the heads of q and k ([W] rope, rope_bwd), in one launch:
+ * pair i of a head (0 <= i < rot / 2) turns by th = positions[t] * f_i,
+ *   x1' = attention_scale * (x1 cos th - x2 sin th)
+ *   x2' = attention_scale * (x2 cos th + x1 sin th)
+ * (x1, x2) = elements (i, i + rot/2), or (2i, 2i + 1) when interleaved; the
+ * elements from rot on are copied.  backward != 0: the gradient, th negated.
+ * fp32 arithmetic, one rounding; the angle is exact to fp32 at any position.
+ *  q, out_q: n_q heads of T tokens, element (t, h, c) at t * tok + h * head + c
+ *  (strides in elements, as given per tensor); k, out_k likewise with n_k heads
+ *  (n_q or n_k may be 0).  An output may be its input (same strides: in place,
+ *  the elements from rot on untouched) or must not overlap it.
+ *  positions [axes, T] int32 (any value); axes > 1: sections (HOST array, axes
+ *  entries, sum rot / 2) gives each axis its consecutive pairs, so tokens can
+ *  carry a time, a height and a width.
+ *  steps [rot / 2] int64: f_i / (2 pi) turns in units of 2^-64 (rounded; scaled
+ *  frequencies for long contexts are just other steps).
+ *  dtype GG_DTYPE_*; D head width, rot even, 0 <= rot <= D, rot <= 1024. */
+int gg_rope(const void* q, int64_t q_tok, int64_t q_head, int n_q, const void* k, int64_t k_tok,
+            int64_t k_head, int n_k, void* out_q, int64_t oq_tok, int64_t oq_head, void* out_k,
+            int64_t ok_tok, int64_t ok_head, const int32_t* positions, int axes,
+            const int32_t* sections, const int64_t* steps, float attention_scale, int64_t T, int D,
+            int rot, int interleaved, int dtype, int backward, void* stream);
 
 #ifdef __cplusplus
 }

@@ -52,6 +52,15 @@ SIGNATURES = {
                             _vp, _vp]),
     "gg_ep_plan": (_int, [_vp, _vp, _int, _int, _vp, _vp, _vp, _vp, _i64]),
     "gg_ep_recv_map": (_int, [_vp, _int, _int, _i64, _vp, _vp, _vp]),
+    "gg_lora_plan_size": (_sz, [_i64, _int]),
+    "gg_lora_plan": (_int, [_vp, _i64, _int, _vp, _sz, _vp, _vp]),
+    "gg_lora_forward": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _int, _int, _i64, _i64, _vp, _vp, _vp,
+                               _vp]),
+    "gg_lora_backward_workspace_size": (_sz, [_i64, _int]),
+    "gg_lora_backward": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _int, _int, _i64, _i64, _vp,
+                                _vp, _vp, _vp, _sz, _vp, _vp]),
+    "gg_rope": (_int, [_vp, _i64, _i64, _int, _vp, _i64, _i64, _int, _vp, _i64, _i64, _vp, _i64, _i64, _vp,
+                       _int, _vp, _vp, ctypes.c_float, _i64, _int, _int, _int, _int, _int, _vp]),
 }
 
 GG_OK = 0
@@ -66,10 +75,17 @@ GG_DEV_BAD_EXPERT_ID = 1
 GG_DEV_BAD_ROW_INDEX = 2
 GG_DEV_SIZES_MISMATCH = 3
 GG_DEV_TIMEOUT = 4
+GG_DEV_BAD_ADAPTER_ID = 5
 GG_MAX_EXPERTS = 2048
 GG_MAX_TOPK = 64
 GG_ROUTE_NOALLOC_SCRATCH_BYTES = 1 << 20
 GG_COMBINE_BF16_MAX_TOPK = 16
+GG_LORA_MAX_RANK = 256
+GG_ROPE_MAX_AXES = 4
+GG_ROPE_MAX_HEADS = 65536
+GG_DTYPE_BF16 = 0
+GG_DTYPE_F16 = 1
+GG_DTYPE_F32 = 2
 GG_OP_ROUTE = 1
 GG_OP_BACKWARD_DW = 2
 GG_OP_FORWARD_COMBINE = 3

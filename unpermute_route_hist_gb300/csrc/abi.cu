@@ -68,9 +68,11 @@ static bool encode(CUtensorMap* m, uint32_t rank, const void* base, const cuuint
         return false;
     }
     const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-    // The swizzle span equals the box's inner extent (rows of 64 or 128 bytes),
+    // The swizzle span equals the box's inner extent (rows of 32, 64 or 128 bytes),
     // which is the layout the MMA descriptors expect for that tile.
-    const CUtensorMapSwizzle sw = box[0] * 2 == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    const CUtensorMapSwizzle sw = box[0] * 2 == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                  : box[0] * 2 == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                     : CU_TENSOR_MAP_SWIZZLE_128B;
     const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base),
                                 dims, strides_bytes, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -179,6 +181,7 @@ const char* gg_device_status_string(int code) {
         case GG_DEV_BAD_ROW_INDEX: return "row index outside its tensor";
         case GG_DEV_SIZES_MISMATCH: return "m_sizes negative or not summing to T*topk";
         case GG_DEV_TIMEOUT: return "a bounded wait inside a kernel ran out";
+        case GG_DEV_BAD_ADAPTER_ID: return "adapter id outside [-1, L)";
         default: return "unknown device status";
     }
 }

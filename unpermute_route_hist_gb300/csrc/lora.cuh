@@ -1,0 +1,181 @@
+// lora.cuh -- what the low-rank adapter kernels share: the plan of a batch's
+// adapter ids (which adapters occur among which rows), masked tensor-core
+// products, and the reads of a cluster partner's shared memory.
+//
+// Low-rank adapters beside a shared projection: token t with adapter a has
+//   U[t] = scale[a] X[t] A[a]^T,   Y[t] = X[t] W^T + U[t] B[a]^T.
+// Rows stay in token order.  The shared product is one dense GEMM; an adapter's
+// part is added to the same accumulator by one masked MMA per (row tile, adapter
+// that occurs in it), whose mask keeps the other rows' accumulators untouched
+// (not multiplied by zero: an infinity in one adapter never reaches another
+// request's rows).
+#pragma once
+
+#include "common.cuh"
+
+namespace gg {
+
+constexpr int kUnit = 256;          // rows of a plan unit (one 2-CTA tile)
+constexpr int kUnitWords = kUnit / 32;
+constexpr int kLoraMaxRank = 256;
+
+// The plan of one batch's ids, as laid out in the caller's buffer.
+//   slots    entries a unit has room for: min(L, 256)
+//   cnt      [units]            adapters that occur in the unit's rows
+//   gid      [units][slots]     those adapters, ascending
+//   mask     [units][slots][8]  the rows of each, a bit a row
+//   start    [units][slots]     rows of that adapter in earlier units
+//   goff     [L + 1]            first position of each adapter's rows in order
+//   order    [T]                rows sorted by adapter, ascending inside one
+struct PlanView {
+    int64_t T;
+    int L, slots;
+    int64_t units;
+    int32_t* cnt;
+    int32_t* gid;
+    uint32_t* mask;
+    int32_t* start;
+    int32_t* goff;
+    int32_t* order;
+};
+
+inline size_t plan_bytes_of(int64_t T, int L) {
+    const int64_t units = (T + kUnit - 1) / kUnit;
+    const int64_t slots = L < kUnit ? L : kUnit;
+    auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
+    return static_cast<size_t>(up(units * 4) + 2 * up(units * slots * 4) + up(units * slots * 32) +
+                               up((static_cast<int64_t>(L) + 1) * 4) + up(T * 4));
+}
+
+inline PlanView plan_view(void* buf, int64_t T, int L) {
+    PlanView v{};
+    v.T = T;
+    v.L = L;
+    v.units = (T + kUnit - 1) / kUnit;
+    v.slots = L < kUnit ? L : kUnit;
+    auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
+    uint8_t* p = static_cast<uint8_t*>(buf);
+    v.cnt = reinterpret_cast<int32_t*>(p);
+    p += up(v.units * 4);
+    v.gid = reinterpret_cast<int32_t*>(p);
+    p += up(v.units * v.slots * 4);
+    v.start = reinterpret_cast<int32_t*>(p);
+    p += up(v.units * v.slots * 4);
+    v.mask = reinterpret_cast<uint32_t*>(p);
+    p += up(v.units * v.slots * 32);
+    v.goff = reinterpret_cast<int32_t*>(p);
+    p += up((static_cast<int64_t>(L) + 1) * 4);
+    v.order = reinterpret_cast<int32_t*>(p);
+    return v;
+}
+
+// Width, in reduction columns, of an adapter's block beside the shared product:
+// the rank rounded up to 16, 32 or 64 (ranks above 64: chunks of 64).  64 / rpad
+// adapters share one stage of the operand ring.
+__host__ __device__ constexpr int rank_pad(int r) { return r <= 16 ? 16 : (r <= 32 ? 32 : 64); }
+
+// Shared-memory descriptor layout code of a K-major tile whose rows are rpad bf16.
+constexpr uint32_t kLayoutSw32 = 6;
+__device__ __forceinline__ uint64_t kmajor_desc(uint32_t addr, int row_bytes) {
+    const uint32_t layout = row_bytes == 32 ? kLayoutSw32 : (row_bytes == 64 ? kLayoutSw64 : kLayoutSw128);
+    return smem_desc(addr, 16, 8 * row_bytes, layout);
+}
+
+// D[tmem] += A[smem] * B[smem]^T for the rows whose mask bit is set; the other
+// rows' accumulators are not written (the MMA's disable-output-lane operand).
+__device__ __forceinline__ void umma_bf16_rows(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               const uint32_t (&keep)[4]) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, 1, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(~keep[0]), "r"(~keep[1]), "r"(~keep[2]), "r"(~keep[3])
+        : "memory");
+}
+__device__ __forceinline__ void umma_bf16_rows_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                    const uint32_t (&keep)[8]) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, 1, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7, %8, %9, %10, %11}, p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(~keep[0]), "r"(~keep[1]), "r"(~keep[2]), "r"(~keep[3]),
+        "r"(~keep[4]), "r"(~keep[5]), "r"(~keep[6]), "r"(~keep[7])
+        : "memory");
+}
+
+// 32 lanes x 8 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// Four floats of a cluster CTA's shared memory (a shared::cluster address).
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t mapa_addr(uint32_t addr, uint32_t cta) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(cta));
+    return remote;
+}
+
+// Programmatic dependent launch: let the next kernel of the stream start its
+// prologue; wait until the previous one has finished and its writes are visible
+// (at once when this kernel was launched without the attribute).
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("fence.proxy.async;" ::: "memory");  // its stores, before this thread's TMA reads of them
+}
+
+// The sum of eight floats at the same shared-memory offset in CTAs 0 .. n-1 of
+// the cluster, in that order.
+__device__ __forceinline__ void cluster_sum8(uint32_t addr, int n, float (&s)[8]) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s[q] = 0.f;
+    for (int c = 0; c < n; ++c) {
+        const uint32_t a = mapa_addr(addr, static_cast<uint32_t>(c));
+        const float4 x = ld_cluster_f32x4(a), y = ld_cluster_f32x4(a + 16);
+        s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
+        s[4] += y.x; s[5] += y.y; s[6] += y.z; s[7] += y.w;
+    }
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&s)[8]) {
+    return make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]),
+                      pack_bf16x2(s[6], s[7]));
+}
+
+// ------------------------------------------------------------------ host --
+
+bool encode_map_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+                   uint64_t row_stride_elems, uint32_t box_inner, uint32_t box_outer);
+bool encode_map_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                   uint64_t stride1_elems, uint64_t stride2_elems, uint32_t b0, uint32_t b1);
+int num_sms();
+
+// U = scale X A^T (B_MN false; A [L, r, K]) or V = scale dY B (B_MN true; B [L, N, r]).
+int lora_shrink_launch(bool b_mn, const uint16_t* X, const uint16_t* ad, const float* scale, const PlanView& plan,
+                       int64_t Kred, int r, uint16_t* out, uint16_t* out_lo, int32_t* status, cudaStream_t st);
+// Y = X W^T + U B^T (b_mn false) or dX = dY W + V A (b_mn true): split-reduction
+// clusters for few row tiles, 2-CTA pair tiles otherwise.
+int lora_project_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, const uint16_t* ad,
+                        const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, int32_t* status,
+                        cudaStream_t st);
+int lora_pair_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, const uint16_t* ad,
+                     const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, int32_t* status,
+                     cudaStream_t st);
+int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, const uint16_t* V, const uint16_t* V_lo,
+                     const PlanView& plan, int64_t K, int64_t N, int r, uint16_t* dA, uint16_t* dB, int32_t* status,
+                     cudaStream_t st);
+int lora_plan_launch(const int32_t* ids, const PlanView& plan, int32_t* status, cudaStream_t st);
+
+}  // namespace gg

@@ -1,0 +1,374 @@
+// lora_pair.cu -- the shared projection with its adapters for batches of many
+// rows: Y = X W^T + U B[a]^T and dX = dY W + V A[a], persistent 2-CTA tiles of
+// 256 x 256 (cta_group::2 tcgen05 MMAs, accumulators double-buffered in tensor
+// memory, TMA-fed six-stage ring).
+//
+// Rows stay in token order: the shared product is one dense GEMM, bound by the
+// tensor rate.  A tile's last ring blocks are its adapters': for each adapter that
+// occurs among the tile's 256 rows one block of rank_pad(r) reduction columns (U's
+// rows against B[a]'s) is accumulated into those rows' lanes alone.  A batch of
+// sequences has one or two adapters a tile, so that adds 1-2 blocks to K / 64.
+// Sorting rows by adapter instead would read and write X and Y once more, or
+// gather X (2.5x slower loads here), and break tiles at every adapter's end.
+//
+// Warp 0: TMA producer; warp 1: tensor memory and, in the even CTA, MMA issue;
+// warps 2-5: epilogue (tensor memory -> bf16 -> 32-byte row pieces).  Every wait
+// is bounded (GG_DEV_TIMEOUT).
+#include <atomic>
+
+#include "lora.cuh"
+
+namespace gg {
+namespace {
+
+constexpr int kPM = 128, kPN = 256, kPK = 64;
+constexpr int kPStages = 6;
+constexpr int kPThreads = 192;
+constexpr int kPSlot = 128 * kPK * 2;  // A rows, or the CTA's half of the B columns
+constexpr int kPStage = 2 * kPSlot;
+constexpr int kPGroup = 8;             // 256-row units of a raster group
+
+struct PairParams {
+    PlanView plan;
+    int Kred, ncols, r, rpad, epb;
+    int ntiles;        // column tiles
+    int64_t tiles;     // all of them
+    uint16_t* out;
+    int st32;          // output rows start 32-byte aligned
+    int32_t* status;
+};
+
+struct PairCtl {
+    uint64_t full[kPStages];
+    uint64_t empty[kPStages];
+    uint64_t tmem_full[2];
+    uint64_t tmem_empty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+constexpr int kPairSmem = 1024 + kPStages * kPStage + sizeof(PairCtl);
+
+// Tile t: groups of kPGroup units sweep every column tile, rows fastest, so the
+// tiles in flight share W's columns and X's rows in L2.
+struct PairTile {
+    int64_t unit;
+    int n0;
+};
+__device__ __forceinline__ PairTile pair_tile(int64_t t, const PairParams& p) {
+    const int64_t per = static_cast<int64_t>(kPGroup) * p.ntiles;
+    const int64_t group = t / per, first = group * kPGroup;
+    const int64_t left = p.plan.units - first;
+    const int h = static_cast<int>(left < kPGroup ? left : kPGroup);
+    const int loc = static_cast<int>(t - group * per);
+    return {first + loc % h, (loc / h) * kPN};
+}
+
+template <bool B_MN>
+__global__ void __launch_bounds__(kPThreads, 1)
+pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+            const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmE, const PairParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    PairCtl* ctl = reinterpret_cast<PairCtl*>(ring + kPStages * kPStage);
+    volatile int* abort_flag = &ctl->abort_flag;
+    const int warp = warp_id(), lane = lane_id();
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int64_t slot = cluster_id_x(), nslot = nclusters_x();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPStages; ++s) {
+            mbar_init(&ctl->full[s], 1);
+            mbar_init(&ctl->empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ctl->tmem_full[b], 1);
+            mbar_init(&ctl->tmem_empty[b], 8);  // the epilogue warps of both CTAs
+        }
+        mbar_init(&ctl->drain, 1);
+        ctl->abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmU);
+        tma_prefetch_desc(&tmE);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(&ctl->tmem_base, 2 * kPN);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    const uint32_t ring0 = smem_u32(ring);
+    const int nb = (p.Kred + kPK - 1) / kPK;
+    const int rchunks = (p.r + 63) / 64;
+    // adapter blocks of a unit with ne entries
+    auto ext_blocks = [&](int ne) { return p.r <= 64 ? (ne + p.epb - 1) / p.epb : ne * rchunks; };
+
+    if (warp == 0) {
+        // ------------------------------------------------------- producer --
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int64_t issued = 0;
+            bool ok = true, waited = false;
+            for (int64_t t = slot; t < p.tiles && ok; t += nslot) {
+                const PairTile ti = pair_tile(t, p);
+                const int32_t arow = static_cast<int32_t>(ti.unit * kUnit + rank * kPM);
+                const int32_t nh = ti.n0 + static_cast<int32_t>(rank) * (kPN / 2);
+                const int ne = p.plan.cnt[ti.unit];
+                const int32_t* gid = p.plan.gid + ti.unit * p.plan.slots;
+                const int total = nb + ext_blocks(ne);
+                for (int i = 0; i < total; ++i) {
+                    if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+                    uint8_t* sA = ring + stage * kPStage;
+                    uint8_t* sB = sA + kPSlot;
+                    const uint32_t bar = mapa_u32(&ctl->full[stage], 0);
+                    if (i < nb) {
+                        const int32_t red = i * kPK;
+                        if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2 * kPStage);
+                        tma_load_2d_pair(sA, &tmX, bar, red, arow);
+                        if (B_MN) {
+                            tma_load_2d_pair(sB, &tmW, bar, nh, red);
+                            tma_load_2d_pair(sB + 8192, &tmW, bar, nh + 64, red);
+                        } else {
+                            tma_load_2d_pair(sB, &tmW, bar, red, nh);
+                        }
+                    } else {
+                        if (!waited) { pdl_wait(); waited = true; }  // U (V) of the kernel before
+                        const int xi = i - nb;
+                        const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
+                        const int en = p.r <= 64 ? min(p.epb, ne - ef) : 1;
+                        const int rc = p.r <= 64 ? 0 : (xi % rchunks) * 64;
+                        const uint32_t eb = 256u * p.rpad;
+                        if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2u * (eb + eb * en));
+                        tma_load_2d_pair(sA, &tmU, bar, rc, arow);
+                        for (int e = 0; e < en; ++e) {
+                            const int g = gid[ef + e];
+                            if (B_MN) {
+                                tma_load_3d_pair(sB + e * eb, &tmE, bar, nh, rc, g);
+                                tma_load_3d_pair(sB + e * eb + eb / 2, &tmE, bar, nh + 64, rc, g);
+                            } else {
+                                tma_load_3d_pair(sB + e * eb, &tmE, bar, rc, nh, g);
+                            }
+                        }
+                    }
+                    ++issued;
+                    if (++stage == kPStages) { stage = 0; phase ^= 1u; }
+                }
+            }
+            if (!waited) pdl_wait();  // the launch before this one has finished before this grid can
+            // The even CTA's barriers count both CTAs' copies: let them land.
+            if (leader) {
+                const int64_t pend = issued < kPStages ? issued : kPStages;
+                for (int64_t j = 0; j < pend; ++j) {
+                    if (--stage < 0) { stage = kPStages - 1; phase ^= 1u; }
+                    int dummy = 0;
+                    mbar_wait(&ctl->full[stage], phase, reinterpret_cast<volatile int*>(&dummy), p.status);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ----------------------------------------------------- MMA issuer --
+        if (leader && lane == 0) {
+            constexpr uint32_t idesc = idesc_bf16_f32(2 * kPM, kPN, 0, B_MN ? 1 : 0);
+            int stage = 0;
+            uint32_t phase = 0, acc = 0;
+            bool ok = true, any_mma = false;
+            for (int64_t t = slot; t < p.tiles && ok; t += nslot, ++acc) {
+                const PairTile ti = pair_tile(t, p);
+                const int ne = p.plan.cnt[ti.unit];
+                const uint32_t* masks = p.plan.mask + ti.unit * p.plan.slots * kUnitWords;
+                const uint32_t buf = acc & 1u;
+                if (!mbar_wait(&ctl->tmem_empty[buf], ((acc >> 1) & 1u) ^ 1u, abort_flag, p.status, 0, kWaitLimitNs,
+                               true))
+                    break;
+                tc_fence_after();
+                const uint32_t d = tmem + buf * kPN;
+                for (int i = 0; i < nb; ++i) {
+                    if (!mbar_wait(&ctl->full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t sA = ring0 + stage * kPStage, sB = sA + kPSlot;
+#pragma unroll
+                    for (int ks = 0; ks < kPK / 16; ++ks) {
+                        const uint64_t ad = smem_desc(sA + ks * 32, 16, 1024, kLayoutSw128);
+                        const uint64_t bd = B_MN ? smem_desc(sB + ks * 2048, 8192, 1024, kLayoutSw128)
+                                                 : smem_desc(sB + ks * 32, 16, 1024, kLayoutSw128);
+                        umma_bf16_pair(d, ad, bd, idesc, (i > 0 || ks > 0) ? 1u : 0u);
+                    }
+                    umma_commit_pair(&ctl->empty[stage], 0x3);
+                    any_mma = true;
+                    if (++stage == kPStages) { stage = 0; phase ^= 1u; }
+                }
+                const int xb = ext_blocks(ne);
+                for (int xi = 0; xi < xb && ok; ++xi) {
+                    const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
+                    const int en = p.r <= 64 ? min(p.epb, ne - ef) : 1;
+                    const int left = p.r <= 64 ? p.r : min(64, p.r - (xi % rchunks) * 64);
+                    const uint32_t eb = 256u * p.rpad;
+                    if (!mbar_wait(&ctl->full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t sA = ring0 + stage * kPStage, sB = sA + kPSlot;
+                    for (int e = 0; e < en; ++e) {
+                        const uint4 m0 = __ldg(reinterpret_cast<const uint4*>(masks + (ef + e) * kUnitWords));
+                        const uint4 m1 = __ldg(reinterpret_cast<const uint4*>(masks + (ef + e) * kUnitWords) + 1);
+                        const uint32_t keep[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+                        for (int ks = 0; ks < (left + 15) / 16; ++ks) {
+                            const uint64_t ad = kmajor_desc(sA + ks * 32, p.rpad * 2);
+                            const uint64_t bd = B_MN ? smem_desc(sB + e * eb + ks * 2048, eb / 2, 1024, kLayoutSw128)
+                                                     : kmajor_desc(sB + e * eb + ks * 32, p.rpad * 2);
+                            umma_bf16_rows_pair(d, ad, bd, idesc, keep);
+                        }
+                    }
+                    umma_commit_pair(&ctl->empty[stage], 0x3);
+                    if (++stage == kPStages) { stage = 0; phase ^= 1u; }
+                }
+                if (ok) umma_commit_pair(&ctl->tmem_full[buf], 0x3);
+            }
+            if (any_mma) {
+                umma_commit_pair(&ctl->drain, 0x1);
+                int dummy = 0;
+                mbar_wait(&ctl->drain, 0, reinterpret_cast<volatile int*>(&dummy), p.status);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------- epilogue --
+        const int q = warp & 3;
+        const uint64_t pol = l2_policy_evict_first();
+        uint32_t acc = 0;
+        for (int64_t t = slot; t < p.tiles; t += nslot, ++acc) {
+            const PairTile ti = pair_tile(t, p);
+            const int64_t row = ti.unit * kUnit + rank * kPM + q * 32 + lane;
+            uint16_t* orow = row < p.plan.T ? p.out + row * p.ncols : nullptr;
+            const uint32_t buf = acc & 1u;
+            if (!warp_wait(&ctl->tmem_full[buf], (acc >> 1) & 1u, abort_flag, p.status, 64, true)) break;
+            tc_fence_after();
+            const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * kPN;
+#pragma unroll 1
+            for (int c = 0; c < kPN; c += 128) {
+                uint32_t v[4][32];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(ta + c + 32 * k, v[k]);
+                tmem_ld_wait();
+                if (c + 128 == kPN) {
+                    // every column is in registers: hand the accumulator back
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (leader) mbar_arrive(&ctl->tmem_empty[buf]);
+                        else mbar_arrive_remote(&ctl->tmem_empty[buf], 0);
+                    }
+                }
+                if (!orow) continue;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int pc = 0; pc < 32; pc += 16) {
+                        const int col = ti.n0 + c + 32 * k + pc;
+                        uint4 o[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t* x = &v[k][pc + 8 * h];
+                            o[h] = make_uint4(pack_bf16x2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                                              pack_bf16x2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                                              pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
+                                              pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
+                        }
+                        if (p.st32 && col + 8 < p.ncols) {
+                            st_global_32_policy(orow + col, o[0], o[1], pol);
+                        } else {
+                            if (col < p.ncols) st_global_16_policy(orow + col, o[0], pol);
+                            if (col + 8 < p.ncols) st_global_16_policy(orow + col + 8, o[1], pol);
+                        }
+                    }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the other may still signal it
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, 2 * kPN);
+}
+
+template <bool B_MN>
+int launch_pair(const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& u, const CUtensorMap& e,
+                const PairParams& p, cudaStream_t st) {
+    auto kern = pair_kernel<B_MN>;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) { record_cuda_error(err); return GG_ERR_CUDA; }
+    if (dev < 0 || dev >= 64) dev = 0;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.blockDim = dim3(kPThreads);
+    cfg.dynamicSmemBytes = kPairSmem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // as many clusters as can be resident at once, asked once per device
+    static std::atomic<int> max_clusters[64];
+    int mc = max_clusters[dev].load(std::memory_order_acquire);
+    if (mc == 0) {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+        if (err != cudaSuccess) { record_cuda_error(err); return GG_ERR_CUDA; }
+        cfg.gridDim = dim3(static_cast<unsigned>(num_sms() & ~1));
+        err = cudaOccupancyMaxActiveClusters(&mc, kern, &cfg);
+        if (err != cudaSuccess || mc < 1) {
+            record_cuda_error(err != cudaSuccess ? err : cudaErrorInvalidConfiguration);
+            return GG_ERR_CUDA;
+        }
+        max_clusters[dev].store(mc, std::memory_order_release);
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (p.tiles < mc ? p.tiles : mc)));
+    cfg.numAttrs = 2;
+    clear_pending_launch_error();
+    err = cudaLaunchKernelEx(&cfg, kern, x, w, u, e, p);
+    if (err != cudaSuccess) { record_cuda_error(err); return GG_ERR_CUDA; }
+    return launch_result();
+}
+
+}  // namespace
+
+int lora_pair_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, const uint16_t* ad,
+                     const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, int32_t* status,
+                     cudaStream_t st) {
+    PairParams p{};
+    p.plan = plan;
+    p.Kred = static_cast<int>(Kred);
+    p.ncols = static_cast<int>(ncols);
+    p.r = r;
+    p.rpad = rank_pad(r);
+    p.epb = 64 / p.rpad;
+    p.ntiles = static_cast<int>((ncols + kPN - 1) / kPN);
+    p.tiles = plan.units * p.ntiles;
+    p.out = out;
+    p.st32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && ncols % 16 == 0;
+    p.status = status;
+    CUtensorMap mX{}, mW{}, mU{}, mE{};
+    if (!encode_map_2d(&mX, X, Kred, plan.T, Kred, kPK, kPM)) return GG_ERR_CUDA;
+    if (!encode_map_2d(&mU, U, r, plan.T, r, p.rpad, kPM)) return GG_ERR_CUDA;
+    if (b_mn) {  // W [Kred, ncols], ad [L, r, ncols]
+        if (!encode_map_2d(&mW, W, ncols, Kred, ncols, 64, kPK)) return GG_ERR_CUDA;
+        if (!encode_map_3d(&mE, ad, ncols, r, plan.L, ncols, ncols * r, 64, p.rpad)) return GG_ERR_CUDA;
+        return launch_pair<true>(mX, mW, mU, mE, p, st);
+    }
+    if (!encode_map_2d(&mW, W, Kred, ncols, Kred, kPK, kPN / 2)) return GG_ERR_CUDA;
+    if (!encode_map_3d(&mE, ad, r, ncols, plan.L, r, ncols * r, p.rpad, kPN / 2)) return GG_ERR_CUDA;
+    return launch_pair<false>(mX, mW, mU, mE, p, st);
+}
+
+}  // namespace gg

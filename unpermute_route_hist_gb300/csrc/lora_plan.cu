@@ -1,0 +1,135 @@
+// lora_plan.cu -- the plan of a batch's adapter ids: for every unit of 256 rows
+// the adapters that occur in it with the rows of each as a bit mask, and all rows
+// sorted by adapter.  Integer work on 4 bytes a token; made once a batch and used
+// by every projection of every layer.  The result is the same on every run: an
+// entry's place is the rank of its adapter id in the unit's bitmap, a row's place
+// the rank of its bit, no atomic hands out places.
+#include "lora.cuh"
+
+namespace gg {
+namespace {
+
+constexpr int kBitWords = GG_MAX_EXPERTS / 32;
+
+// One CTA of 256 threads per unit, a thread per row.
+__global__ void __launch_bounds__(kUnit) plan_units_kernel(const int32_t* __restrict__ ids, PlanView v, int32_t* status) {
+    __shared__ uint32_t bits[kBitWords];     // adapters that occur
+    __shared__ int32_t before[kBitWords];    // occurring adapters in earlier words
+    __shared__ uint32_t rows[kUnit][kUnitWords];
+    const int64_t u = blockIdx.x;
+    const int tid = threadIdx.x;
+    const int64_t t = u * kUnit + tid;
+    for (int i = tid; i < kBitWords; i += kUnit) bits[i] = 0;
+    for (int i = tid; i < kUnit * kUnitWords; i += kUnit) (&rows[0][0])[i] = 0;
+    __syncthreads();
+    int a = t < v.T ? ids[t] : -1;
+    if (a < -1 || a >= v.L) {
+        set_status(status, GG_DEV_BAD_ADAPTER_ID);
+        a = -1;
+    }
+    if (a >= 0) atomicOr(&bits[a >> 5], 1u << (a & 31));
+    __syncthreads();
+    if (tid < 32) {  // exclusive prefix of the words' counts: two words a lane
+        static_assert(kBitWords == 64, "two bitmap words a lane");
+        const int c0 = __popc(bits[2 * tid]), c1 = __popc(bits[2 * tid + 1]);
+        int x = c0 + c1;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, d);
+            if (tid >= d) x += y;
+        }
+        before[2 * tid] = x - c0 - c1;
+        before[2 * tid + 1] = x - c1;
+        if (tid == 31) v.cnt[u] = x;
+    }
+    __syncthreads();
+    if (a >= 0) {
+        const int j = before[a >> 5] + __popc(bits[a >> 5] & ((1u << (a & 31)) - 1u));
+        atomicOr(&rows[j][tid >> 5], 1u << (tid & 31));
+        v.gid[u * v.slots + j] = a;  // the same value from every row of the adapter
+    }
+    __syncthreads();
+    const int n = before[kBitWords - 1] + __popc(bits[kBitWords - 1]);
+    for (int i = tid; i < n * kUnitWords; i += kUnit)
+        v.mask[u * v.slots * kUnitWords + i] = (&rows[0][0])[i];
+}
+
+// One warp per adapter: its rows in each unit, summed in unit order into start;
+// goff[a + 1] receives its total (the scan below makes offsets of them).
+__global__ void __launch_bounds__(128) plan_groups_kernel(PlanView v) {
+    const int a = static_cast<int>((static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5);
+    const int lane = lane_id();
+    if (a >= v.L) return;
+    int run = 0;
+    for (int64_t u0 = 0; u0 < v.units; u0 += 32) {
+        const int64_t u = u0 + lane;
+        int c = 0;
+        int64_t at = -1;
+        if (u < v.units) {
+            int lo = 0, hi = v.cnt[u];
+            const int32_t* g = v.gid + u * v.slots;
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (g[mid] < a) lo = mid + 1; else hi = mid;
+            }
+            if (lo < v.cnt[u] && g[lo] == a) {
+                at = u * v.slots + lo;
+                for (int w = 0; w < kUnitWords; ++w) c += __popc(v.mask[at * kUnitWords + w]);
+            }
+        }
+        int x = c;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        if (at >= 0) v.start[at] = run + x - c;
+        run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) v.goff[a + 1] = run;
+}
+
+// One warp: exclusive prefix of the adapters' row counts, in place.
+__global__ void __launch_bounds__(32) plan_scan_kernel(PlanView v) {
+    const int lane = lane_id();
+    int run = 0;
+    for (int a0 = 0; a0 < v.L; a0 += 32) {
+        const int a = a0 + lane;
+        int x = a < v.L ? v.goff[a + 1] : 0;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        if (a < v.L) v.goff[a + 1] = run + x;
+        run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) v.goff[0] = 0;
+}
+
+// Rows into adapter order: one CTA per unit, a warp per entry in turn, each lane
+// placing its bit of every mask word.
+__global__ void __launch_bounds__(kUnit) plan_order_kernel(PlanView v) {
+    const int64_t u = blockIdx.x;
+    const int lane = lane_id();
+    for (int j = warp_id(); j < v.cnt[u]; j += kUnit / 32) {
+        const int64_t at = u * v.slots + j;
+        int32_t pos = v.goff[v.gid[at]] + v.start[at];
+        for (int w = 0; w < kUnitWords; ++w) {
+            const uint32_t m = v.mask[at * kUnitWords + w];
+            if ((m >> lane) & 1u)
+                v.order[pos + __popc(m & ((1u << lane) - 1u))] = static_cast<int32_t>(u * kUnit + w * 32 + lane);
+            pos += __popc(m);
+        }
+    }
+}
+
+}  // namespace
+
+int lora_plan_launch(const int32_t* ids, const PlanView& v, int32_t* status, cudaStream_t st) {
+    clear_pending_launch_error();
+    plan_units_kernel<<<static_cast<unsigned>(v.units), kUnit, 0, st>>>(ids, v, status);
+    plan_groups_kernel<<<static_cast<unsigned>((v.L + 3) / 4), 128, 0, st>>>(v);
+    plan_scan_kernel<<<1, 32, 0, st>>>(v);
+    plan_order_kernel<<<static_cast<unsigned>(v.units), kUnit, 0, st>>>(v);
+    return launch_result();
+}
+
+}  // namespace gg
