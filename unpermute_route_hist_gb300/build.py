@@ -21,7 +21,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libgg.so")
 
 SOURCES = ["abi.cu", "route.cu", "route_noalloc.cu", "move.cu", "gemm_ragged_m.cu", "gemm_dw.cu", "gemm_dual.cu", "ep.cu",
-           "lora.cu", "lora_plan.cu", "lora_rows.cu", "lora_pair.cu", "lora_grad.cu", "rope.cu"]
+           "lora.cu", "lora_plan.cu", "lora_shrink.cu", "lora_project.cu", "lora_pair.cu", "lora_grad.cu", "rope.cu"]
 HEADERS = ["common.cuh", "gemm_engine.cuh", "gemm_launch.cuh", "lora.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

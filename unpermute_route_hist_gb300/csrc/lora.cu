@@ -1,6 +1,6 @@
 // lora.cu -- entry points of the low-rank adapters beside a shared projection:
 // argument checks and the order of the launches.  The kernels are in lora_plan.cu
-// (the batch's plan), lora_rows.cu (low-rank products, few-row projections),
+// (the batch's plan), lora_shrink.cu (low-rank products), lora_project.cu (projections of few rows),
 // lora_pair.cu (projections of many rows) and lora_grad.cu (adapter gradients).
 #include "lora.cuh"
 

@@ -11,6 +11,8 @@
 // request's rows).
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace gg {
@@ -21,52 +23,67 @@ constexpr int kLoraMaxRank = 256;
 
 // The plan of one batch's ids, as laid out in the caller's buffer.
 //   slots    entries a unit has room for: min(L, 256)
+//   ntile    [1]                row tiles in adapter order (below)
 //   cnt      [units]            adapters that occur in the unit's rows
 //   gid      [units][slots]     those adapters, ascending
 //   mask     [units][slots][8]  the rows of each, a bit a row
+//   any      [units][8]         the rows that have an adapter
 //   start    [units][slots]     rows of that adapter in earlier units
 //   goff     [L + 1]            first position of each adapter's rows in order
+//   toff     [L + 1]            first tile of each adapter
 //   order    [T]                rows sorted by adapter, ascending inside one
+//   tile     [max_tiles] int4   {adapter, position in order, rows, first row if the
+//                               rows are neighbours in memory, else -1}: up to 128
+//                               rows of one adapter
 struct PlanView {
     int64_t T;
     int L, slots;
-    int64_t units;
+    int64_t units, max_tiles;
+    int32_t* ntile;
     int32_t* cnt;
     int32_t* gid;
     uint32_t* mask;
+    uint32_t* any;
     int32_t* start;
     int32_t* goff;
+    int32_t* toff;
     int32_t* order;
+    int4* tile;
 };
 
-inline size_t plan_bytes_of(int64_t T, int L) {
-    const int64_t units = (T + kUnit - 1) / kUnit;
-    const int64_t slots = L < kUnit ? L : kUnit;
-    auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
-    return static_cast<size_t>(up(units * 4) + 2 * up(units * slots * 4) + up(units * slots * 32) +
-                               up((static_cast<int64_t>(L) + 1) * 4) + up(T * 4));
-}
+constexpr int kTileRows = 128;
 
-inline PlanView plan_view(void* buf, int64_t T, int L) {
+// The plan's layout over buf (null: only the size matters); its bytes in *bytes.
+inline PlanView plan_view(void* buf, int64_t T, int L, size_t* bytes = nullptr) {
     PlanView v{};
     v.T = T;
     v.L = L;
     v.units = (T + kUnit - 1) / kUnit;
     v.slots = L < kUnit ? L : kUnit;
-    auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
-    uint8_t* p = static_cast<uint8_t*>(buf);
-    v.cnt = reinterpret_cast<int32_t*>(p);
-    p += up(v.units * 4);
-    v.gid = reinterpret_cast<int32_t*>(p);
-    p += up(v.units * v.slots * 4);
-    v.start = reinterpret_cast<int32_t*>(p);
-    p += up(v.units * v.slots * 4);
-    v.mask = reinterpret_cast<uint32_t*>(p);
-    p += up(v.units * v.slots * 32);
-    v.goff = reinterpret_cast<int32_t*>(p);
-    p += up((static_cast<int64_t>(L) + 1) * 4);
-    v.order = reinterpret_cast<int32_t*>(p);
+    v.max_tiles = T / kTileRows + (T < L ? T : L);
+    size_t at = 0;
+    auto take = [&](int64_t n, int64_t size) {
+        void* p = static_cast<uint8_t*>(buf) + at;
+        at += static_cast<size_t>((n * size + 255) / 256 * 256);
+        return p;
+    };
+    v.ntile = static_cast<int32_t*>(take(1, 4));
+    v.cnt = static_cast<int32_t*>(take(v.units, 4));
+    v.gid = static_cast<int32_t*>(take(v.units * v.slots, 4));
+    v.mask = static_cast<uint32_t*>(take(v.units * v.slots, 32));
+    v.any = static_cast<uint32_t*>(take(v.units, 32));
+    v.start = static_cast<int32_t*>(take(v.units * v.slots, 4));
+    v.goff = static_cast<int32_t*>(take(static_cast<int64_t>(L) + 1, 4));
+    v.toff = static_cast<int32_t*>(take(static_cast<int64_t>(L) + 1, 4));
+    v.order = static_cast<int32_t*>(take(T, 4));
+    v.tile = static_cast<int4*>(take(v.max_tiles, 16));
+    if (bytes) *bytes = at;
     return v;
+}
+inline size_t plan_bytes_of(int64_t T, int L) {
+    size_t b = 0;
+    plan_view(nullptr, T, L, &b);
+    return b;
 }
 
 // Width, in reduction columns, of an adapter's block beside the shared product:
@@ -79,6 +96,18 @@ constexpr uint32_t kLayoutSw32 = 6;
 __device__ __forceinline__ uint64_t kmajor_desc(uint32_t addr, int row_bytes) {
     const uint32_t layout = row_bytes == 32 ? kLayoutSw32 : (row_bytes == 64 ? kLayoutSw64 : kLayoutSw128);
     return smem_desc(addr, 16, 8 * row_bytes, layout);
+}
+
+// The same for an operand read along its columns (MN-major): reduction rows of
+// row_bytes (32, 64 or 128), chunks of that width chunk_bytes apart.
+__device__ __forceinline__ uint64_t mnmajor_desc(uint32_t addr, int row_bytes, uint32_t chunk_bytes) {
+    const uint32_t layout = row_bytes == 32 ? kLayoutSw32 : (row_bytes == 64 ? kLayoutSw64 : kLayoutSw128);
+    return smem_desc(addr, chunk_bytes, 8 * row_bytes, layout);
+}
+
+// idesc_bf16_f32 for a column count known at run time.
+__device__ __forceinline__ uint32_t idesc_bf16_f32_n(int M, int N, int a_mn_major, int b_mn_major) {
+    return (idesc_bf16_f32(M, 0, a_mn_major, b_mn_major)) | (static_cast<uint32_t>(N >> 3) << 17);
 }
 
 // D[tmem] += A[smem] * B[smem]^T for the rows whose mask bit is set; the other
@@ -137,15 +166,25 @@ __device__ __forceinline__ void pdl_wait() {
 }
 
 // The sum of eight floats at the same shared-memory offset in CTAs 0 .. n-1 of
-// the cluster, in that order.
+// the cluster (at most 8), in that order; all reads are in flight together.
 __device__ __forceinline__ void cluster_sum8(uint32_t addr, int n, float (&s)[8]) {
+    float4 x[8], y[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        if (c < n) {
+            const uint32_t a = mapa_addr(addr, static_cast<uint32_t>(c));
+            x[c] = ld_cluster_f32x4(a);
+            y[c] = ld_cluster_f32x4(a + 16);
+        }
+    }
 #pragma unroll
     for (int q = 0; q < 8; ++q) s[q] = 0.f;
-    for (int c = 0; c < n; ++c) {
-        const uint32_t a = mapa_addr(addr, static_cast<uint32_t>(c));
-        const float4 x = ld_cluster_f32x4(a), y = ld_cluster_f32x4(a + 16);
-        s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
-        s[4] += y.x; s[5] += y.y; s[6] += y.z; s[7] += y.w;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        if (c < n) {
+            s[0] += x[c].x; s[1] += x[c].y; s[2] += x[c].z; s[3] += x[c].w;
+            s[4] += y[c].x; s[5] += y[c].y; s[6] += y[c].z; s[7] += y[c].w;
+        }
     }
 }
 
@@ -161,6 +200,62 @@ bool encode_map_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t ou
 bool encode_map_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                    uint64_t stride1_elems, uint64_t stride2_elems, uint32_t b0, uint32_t b1);
 int num_sms();
+
+// Launch of a kernel in clusters of S CTAs.
+struct ClusterLaunch {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    ClusterLaunch(int64_t grid, int threads, size_t smem, int S, bool after_start, cudaStream_t st) : cfg{} {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(S);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        // may start while the kernel before it runs (griddepcontrol)
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(grid));
+        cfg.blockDim = dim3(static_cast<unsigned>(threads));
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cfg.attrs = attr;
+        cfg.numAttrs = after_start ? 2 : 1;
+    }
+    ClusterLaunch(const ClusterLaunch&) = delete;
+};
+
+constexpr int kMaxCluster = 8;
+
+// Per kernel: the shared-memory opt-in and how many clusters of 1 .. 8 CTAs are
+// resident at once with smem bytes, asked once per device.  GG_OK or an error code.
+struct ClusterRoom {
+    std::atomic<int> n[64][kMaxCluster + 1];  // 0: not asked yet
+    template <typename K>
+    int get(K kern, int threads, size_t smem, const int** room) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) { record_cuda_error(e); return GG_ERR_CUDA; }
+        if (dev < 0 || dev >= 64) dev = 0;
+        static thread_local int out[kMaxCluster + 1];
+        if (n[dev][kMaxCluster].load(std::memory_order_acquire) == 0) {
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            for (int S = 1; S <= kMaxCluster && e == cudaSuccess; ++S) {
+                ClusterLaunch l(int64_t(S) * 1024, threads, smem, S, false, nullptr);
+                int c = 0;
+                e = cudaOccupancyMaxActiveClusters(&c, kern, &l.cfg);
+                if (e == cudaSuccess && c < 1) e = cudaErrorInvalidConfiguration;
+                n[dev][S].store(c, std::memory_order_release);
+            }
+            if (e != cudaSuccess) {
+                n[dev][kMaxCluster].store(0, std::memory_order_release);
+                record_cuda_error(e);
+                return GG_ERR_CUDA;
+            }
+        }
+        for (int S = 1; S <= kMaxCluster; ++S) out[S] = n[dev][S].load(std::memory_order_acquire);
+        *room = out;
+        return GG_OK;
+    }
+};
 
 // U = scale X A^T (B_MN false; A [L, r, K]) or V = scale dY B (B_MN true; B [L, N, r]).
 int lora_shrink_launch(bool b_mn, const uint16_t* X, const uint16_t* ad, const float* scale, const PlanView& plan,

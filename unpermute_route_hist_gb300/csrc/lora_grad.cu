@@ -5,15 +5,13 @@
 // Both are one problem: a wide source (X, dY) read along its columns against a
 // narrow one (V, U), for a 128-column chunk of the wide source and one adapter.
 // Bound by reading X and dY once; the MMAs run with the wide columns as M and the
-// rank (padded to 64) as N.
+// rank as N.
 //
-// The rows are the plan's order: 64 rows of one adapter a block.  A block whose
+// The rows are the plan's tiles, in blocks of 64 rows of one adapter.  A block whose
 // rows are neighbours in memory (a sequence's) is copied by TMA; any other (ids
 // in no order, the adapter's last rows) is gathered row by row with cp.async, rows
 // past the end as zeros, so nothing of another adapter's rows enters the sums.
-// Blocks are split over a cluster and the partial sums joined as in lora_rows.cu.
-#include <atomic>
-
+// Blocks are split over a cluster and the partial sums joined as in lora_shrink.cu.
 #include "lora.cuh"
 
 namespace gg {
@@ -23,9 +21,11 @@ constexpr int kGM = 128;            // columns of the wide source
 constexpr int kGK = 64;             // rows of a block
 constexpr int kGThreads = 192;      // producer, issuer, four gather / epilogue warps
 constexpr int kGWide = kGM * kGK * 2;
-constexpr int kGNarrow = 64 * kGK * 2;  // 64 rank columns of a block
 constexpr int kGMaxStages = 6;
-constexpr int kGMaxCluster = 8;
+// the partial sums (rank up to 64: two CTAs an SM) fit the drained ring
+static_assert(98304 >= 4 * kGM * (64 + 4) && 98304 >= 4 * 64 * (kGM + 4), "ring");
+static_assert(196608 >= 4 * kGM * (kLoraMaxRank + 4) && 196608 >= 4 * kLoraMaxRank * (kGM + 4), "ring");
+
 
 struct GradSide {
     const uint16_t* wide;      // [T, cols]
@@ -39,7 +39,7 @@ struct GradSide {
 struct GradParams {
     PlanView plan;
     GradSide side[2];          // dA, dB
-    int r, nc;                 // rank, 64-column pieces of it
+    int r, chunk, nc;          // rank; width (16, 32, 64) and number of its pieces
     int stages;
     int stage_bytes;
     int32_t* status;
@@ -58,7 +58,9 @@ struct GradMaps {
     CUtensorMap narrow[3];     // V, V's remainder, U
 };
 
-__global__ void __launch_bounds__(kGThreads, 2)
+// RING: bytes of the operand ring (two CTAs an SM, or one)
+template <int RING>
+__global__ void __launch_bounds__(kGThreads, RING > 98304 ? 1 : 2)
 grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int S) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -75,7 +77,8 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int
     const int sd = tile < p.side[0].tiles ? 0 : 1;
     const GradSide side = p.side[sd];
     const int col0 = (sd == 0 ? tile : tile - p.side[0].tiles) * kGM;
-    const int ncols = 64 * p.nc;  // accumulator columns
+    const int ncols = p.chunk * p.nc;  // accumulator columns
+    const uint32_t piece_bytes = static_cast<uint32_t>(p.chunk) * kGK * 2;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -87,7 +90,7 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int
         fence_barrier_init();
         tma_prefetch_desc(&maps.wide[sd]);
     }
-    const int tcols = p.nc == 1 ? 64 : (p.nc == 2 ? 128 : 256);
+    const int tcols = ncols <= 32 ? 32 : (ncols <= 64 ? 64 : (ncols <= 128 ? 128 : 256));
     if (warp == 1) {
         tmem_alloc(&ctl->tmem_base, tcols);
         tmem_relinquish();
@@ -95,9 +98,8 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const int32_t g0 = p.plan.goff[a];
-    const int count = p.plan.goff[a + 1] - g0;
-    const int32_t* order = p.plan.order + g0;
+    const int count = p.plan.goff[a + 1] - p.plan.goff[a];
+    const int4* tiles_a = p.plan.tile + p.plan.toff[a];
     const int nb = (count + kGK - 1) / kGK;
     const int act = min(S, nb);  // ranks with blocks
     const int lo = rank < act ? static_cast<int>(static_cast<int64_t>(nb) * rank / act) : 0;
@@ -105,8 +107,21 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int
     const uint32_t tmem = ctl->tmem_base;
     const uint32_t ring0 = smem_u32(ring);
     const int nnarrow = p.nc * side.parts;
-    // 64 neighbouring rows: their first and last are 63 apart (order ascends)
-    auto in_a_row = [&](int b) { return (b + 1) * kGK <= count && order[b * kGK + kGK - 1] - order[b * kGK] == kGK - 1; };
+    // Block b is half b & 1 of tile b / 2.  Each role walks the tiles with the next
+    // one's entry already loaded.
+    static_assert(kTileRows == 2 * kGK, "two blocks a tile");
+    int4 cur = make_int4(0, 0, 0, 0), next = cur;
+    if (hi > lo) {
+        cur = tiles_a[lo / 2];
+        if (lo / 2 < (hi - 1) / 2) next = tiles_a[lo / 2 + 1];
+    }
+    auto advance = [&](int b) {  // to block b + 1
+        if ((b & 1) && b + 1 < hi) {
+            cur = next;
+            if ((b + 1) / 2 < (hi - 1) / 2) next = tiles_a[(b + 1) / 2 + 1];
+        }
+    };
+    auto by_tma = [&](int b) { return cur.w >= 0 && cur.z >= ((b & 1) + 1) * kGK; };
 
     if (warp == 0) {
         // --------------------------------------------------- TMA producer --
@@ -116,18 +131,19 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int
             for (int b = lo; b < hi; ++b) {
                 if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) break;
                 uint64_t* bar = &ctl->full[stage];
-                if (in_a_row(b)) {
+                if (by_tma(b)) {
                     uint8_t* s = ring + stage * p.stage_bytes;
-                    const int32_t t = order[b * kGK];
-                    mbar_arrive_expect_tx(bar, kGWide + kGNarrow * nnarrow);
+                    const int32_t t = cur.w + (b & 1) * kGK;
+                    mbar_arrive_expect_tx(bar, kGWide + piece_bytes * nnarrow);
                     tma_load_2d(s, &maps.wide[sd], bar, col0, t);
                     tma_load_2d(s + kGWide / 2, &maps.wide[sd], bar, col0 + 64, t);
                     for (int k = 0; k < nnarrow; ++k)
-                        tma_load_2d(s + kGWide + k * kGNarrow, &maps.narrow[sd == 0 ? k / p.nc : 2], bar,
-                                    (k % p.nc) * 64, t);
+                        tma_load_2d(s + kGWide + k * piece_bytes, &maps.narrow[sd == 0 ? k / p.nc : 2], bar,
+                                    (k % p.nc) * p.chunk, t);
                 } else {
                     mbar_arrive(bar);
                 }
+                advance(b);
                 ++issued;
                 if (++stage == p.stages) { stage = 0; phase ^= 1u; }
             }
@@ -142,7 +158,7 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int
     } else if (warp == 1) {
         // ----------------------------------------------------- MMA issuer --
         if (lane == 0 && hi > lo) {
-            const uint32_t idesc = idesc_bf16_f32(kGM, 16, 1, 1) - (2u << 17) + (static_cast<uint32_t>(ncols >> 3) << 17);
+            const uint32_t idesc = idesc_bf16_f32_n(kGM, ncols, 1, 1);
             int stage = 0;
             uint32_t phase = 0;
             bool any_mma = false;
@@ -152,11 +168,11 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int
                 fence_proxy_async_smem();  // gathered rows are generic-proxy writes
                 const uint32_t s = ring0 + stage * p.stage_bytes;
                 for (int part = 0; part < side.parts; ++part) {
-                    const uint32_t sN = s + kGWide + part * p.nc * kGNarrow;
+                    const uint32_t sN = s + kGWide + part * p.nc * piece_bytes;
 #pragma unroll
                     for (int ks = 0; ks < kGK / 16; ++ks)
                         umma_bf16(tmem, smem_desc(s + ks * 2048, kGWide / 2, 1024, kLayoutSw128),
-                                  smem_desc(sN + ks * 2048, kGNarrow, 1024, kLayoutSw128), idesc,
+                                  mnmajor_desc(sN + ks * 32 * p.chunk, 2 * p.chunk, piece_bytes), idesc,
                                   (b > lo || part > 0 || ks > 0) ? 1u : 0u);
                 }
                 umma_commit(&ctl->empty[stage]);
@@ -174,19 +190,20 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int
         uint32_t phase = 0;
         for (int b = lo; b < hi; ++b) {
             if (!warp_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status, 32)) break;
-            if (in_a_row(b)) {
+            if (by_tma(b)) {
                 mbar_arrive(&ctl->full[stage]);
             } else {
                 const uint32_t s = ring0 + stage * p.stage_bytes;
+                const int off = (b & 1) * kGK, valid = cur.z - off;
+                auto token = [&](int rr) {  // of the block's row rr
+                    return rr >= valid ? -1 : (cur.w >= 0 ? cur.w + off + rr : p.plan.order[cur.y + off + rr]);
+                };
                 // 16 pieces of 8 columns a row of the wide source, 8 rows a step
                 const int pc = gt & 15;
                 const bool in = col0 + pc * 8 < side.cols;
                 int32_t tok[kGK / 8];
 #pragma unroll
-                for (int j = 0; j < kGK / 8; ++j) {
-                    const int rr = (gt >> 4) + 8 * j;
-                    tok[j] = b * kGK + rr < count ? order[b * kGK + rr] : -1;
-                }
+                for (int j = 0; j < kGK / 8; ++j) tok[j] = token((gt >> 4) + 8 * j);
 #pragma unroll
                 for (int j = 0; j < kGK / 8; ++j) {
                     const int rr = (gt >> 4) + 8 * j;
@@ -195,22 +212,24 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int
                                 v ? side.wide + static_cast<int64_t>(tok[j]) * side.cols + col0 + pc * 8 : side.wide,
                                 v ? 16u : 0u);
                 }
-                // narrow: 8 pieces a row and 64-column piece, 16 rows a step
-                const int np = gt & 7;
-#pragma unroll
-                for (int j = 0; j < kGK / 16; ++j) {
-                    const int rr = (gt >> 3) + 16 * j;
-                    const int32_t t = b * kGK + rr < count ? order[b * kGK + rr] : -1;
+                // narrow: chunk / 8 pieces a row, swizzled over the row's width as TMA does
+                // (16-byte piece index XOR address bits 7 and up)
+                const int npc = p.chunk / 8;
+                const int np = gt % npc, rows_a_step = 128 / npc;
+                for (int rr = gt / npc; rr < kGK; rr += rows_a_step) {
+                    const int32_t t = token(rr);
+                    const uint32_t flip = static_cast<uint32_t>((rr * p.chunk * 2) >> 7) & (npc - 1);
                     for (int k = 0; k < nnarrow; ++k) {
-                        const int c = (k % p.nc) * 64 + np * 8;
+                        const int c = (k % p.nc) * p.chunk + np * 8;
                         const uint16_t* src = side.narrow[k / p.nc];
                         const bool v = t >= 0 && c < p.r;
-                        cp_async_16(s + kGWide + k * kGNarrow + rr * 128 + ((np ^ (rr & 7)) << 4),
+                        cp_async_16(s + kGWide + k * piece_bytes + rr * p.chunk * 2 + ((np ^ flip) << 4),
                                     v ? src + static_cast<int64_t>(t) * p.r + c : src, v ? 16u : 0u);
                     }
                 }
                 cp_async_mbar_arrive(&ctl->full[stage]);
             }
+            advance(b);
             if (++stage == p.stages) { stage = 0; phase ^= 1u; }
         }
         cp_async_wait<0>();
@@ -272,6 +291,29 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int
     }
 }
 
+template <int RING>
+int launch_grad(const GradMaps& m, GradParams p, cudaStream_t st) {
+    constexpr size_t smem = 1024 + RING;
+    static ClusterRoom rooms;
+    const int* room = nullptr;
+    const int rc = rooms.get(grad_kernel<RING>, kGThreads, smem, &room);
+    if (rc != GG_OK) return rc;
+    p.stages = RING / p.stage_bytes;
+    if (p.stages > kGMaxStages) p.stages = kGMaxStages;
+    // The split: until the CTAs fill the GPU twice, at least two blocks of a mean
+    // adapter each.
+    const int64_t items = static_cast<int64_t>(p.plan.L) * (p.side[0].tiles + p.side[1].tiles);
+    const int64_t blocks = p.plan.T / kGK / p.plan.L;
+    int S = kMaxCluster;
+    while (S > 1 && (items > 2 * room[S] || S * 2 > blocks)) S /= 2;
+    if (items * S >= (int64_t(1) << 31)) return GG_ERR_UNSUPPORTED;
+    ClusterLaunch l(items * S, kGThreads, smem, S, false, st);
+    clear_pending_launch_error();
+    const cudaError_t err = cudaLaunchKernelEx(&l.cfg, grad_kernel<RING>, m, p, S);
+    if (err != cudaSuccess) { record_cuda_error(err); return GG_ERR_CUDA; }
+    return launch_result();
+}
+
 }  // namespace
 
 int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, const uint16_t* V, const uint16_t* V_lo,
@@ -280,62 +322,26 @@ int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, c
     GradParams p{};
     p.plan = plan;
     p.r = r;
-    p.nc = (r + 63) / 64;
+    p.chunk = rank_pad(r);
+    p.nc = (r + p.chunk - 1) / p.chunk;
     p.status = status;
     if (dA)
         p.side[0] = GradSide{X, {V, V_lo}, 2, static_cast<int>(K), static_cast<int>((K + kGM - 1) / kGM), dA};
     if (dB)
         p.side[1] = GradSide{dY, {U, nullptr}, 1, static_cast<int>(N), static_cast<int>((N + kGM - 1) / kGM), dB};
-    p.stage_bytes = kGWide + kGNarrow * p.nc * (dA ? 2 : 1);
-    // two CTAs an SM for ranks up to 64, one above; the partial sums reuse the ring
-    const int room = p.nc == 1 ? 98304 : 196608;
-    p.stages = room / p.stage_bytes;
-    if (p.stages > kGMaxStages) p.stages = kGMaxStages;
-    int smem = p.stages * p.stage_bytes;
-    const int sums = 4 * (r * (kGM + 4) > kGM * (r + 4) ? r * (kGM + 4) : kGM * (r + 4));
-    if (smem < sums) smem = sums;
-    smem += 1024;
-    const int64_t items = static_cast<int64_t>(plan.L) * (p.side[0].tiles + p.side[1].tiles);
-    const int64_t blocks = plan.T / kGK / plan.L;  // of a mean adapter
-    int S = kGMaxCluster;
-    while (S > 1 && (items * S > 4 * num_sms() || S * 2 > blocks)) S /= 2;
-    if (items * S >= (int64_t(1) << 31)) return GG_ERR_UNSUPPORTED;
+    p.stage_bytes = kGWide + p.chunk * kGK * 2 * p.nc * (dA ? 2 : 1);
     GradMaps m{};
     if (dA) {
         if (!encode_map_2d(&m.wide[0], X, K, plan.T, K, 64, kGK)) return GG_ERR_CUDA;
-        if (!encode_map_2d(&m.narrow[0], V, r, plan.T, r, 64, kGK)) return GG_ERR_CUDA;
-        if (!encode_map_2d(&m.narrow[1], V_lo, r, plan.T, r, 64, kGK)) return GG_ERR_CUDA;
+        if (!encode_map_2d(&m.narrow[0], V, r, plan.T, r, p.chunk, kGK)) return GG_ERR_CUDA;
+        if (!encode_map_2d(&m.narrow[1], V_lo, r, plan.T, r, p.chunk, kGK)) return GG_ERR_CUDA;
     }
     if (dB) {
         if (!encode_map_2d(&m.wide[1], dY, N, plan.T, N, 64, kGK)) return GG_ERR_CUDA;
-        if (!encode_map_2d(&m.narrow[2], U, r, plan.T, r, 64, kGK)) return GG_ERR_CUDA;
+        if (!encode_map_2d(&m.narrow[2], U, r, plan.T, r, p.chunk, kGK)) return GG_ERR_CUDA;
     }
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) { record_cuda_error(err); return GG_ERR_CUDA; }
-    if (dev < 0 || dev >= 64) dev = 0;
-    static std::atomic<bool> smem_set[64];
-    if (!smem_set[dev].load(std::memory_order_acquire)) {
-        err = cudaFuncSetAttribute(grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-        if (err != cudaSuccess) { record_cuda_error(err); return GG_ERR_CUDA; }
-        smem_set[dev].store(true, std::memory_order_release);
-    }
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(S);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(items * S));
-    cfg.blockDim = dim3(kGThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    clear_pending_launch_error();
-    err = cudaLaunchKernelEx(&cfg, grad_kernel, m, p, S);
-    if (err != cudaSuccess) { record_cuda_error(err); return GG_ERR_CUDA; }
-    return launch_result();
+    // two CTAs an SM for ranks up to 64, one above
+    return p.nc == 1 ? launch_grad<98304>(m, p, st) : launch_grad<196608>(m, p, st);
 }
 
 }  // namespace gg

@@ -51,6 +51,8 @@ __global__ void __launch_bounds__(kUnit) plan_units_kernel(const int32_t* __rest
     const int n = before[kBitWords - 1] + __popc(bits[kBitWords - 1]);
     for (int i = tid; i < n * kUnitWords; i += kUnit)
         v.mask[u * v.slots * kUnitWords + i] = (&rows[0][0])[i];
+    const uint32_t with = __ballot_sync(0xffffffffu, a >= 0);
+    if ((tid & 31) == 0) v.any[u * kUnitWords + (tid >> 5)] = with;
 }
 
 // One warp per adapter: its rows in each unit, summed in unit order into start;
@@ -87,21 +89,33 @@ __global__ void __launch_bounds__(128) plan_groups_kernel(PlanView v) {
     if (lane == 0) v.goff[a + 1] = run;
 }
 
-// One warp: exclusive prefix of the adapters' row counts, in place.
+// One warp: exclusive prefixes of the adapters' row counts (in place) and tiles.
 __global__ void __launch_bounds__(32) plan_scan_kernel(PlanView v) {
     const int lane = lane_id();
-    int run = 0;
+    int rows = 0, tiles = 0;
     for (int a0 = 0; a0 < v.L; a0 += 32) {
         const int a = a0 + lane;
-        int x = a < v.L ? v.goff[a + 1] : 0;
+        const int c = a < v.L ? v.goff[a + 1] : 0;
+        int x = c, y = (c + kTileRows - 1) / kTileRows;
         for (int d = 1; d < 32; d <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += y;
+            const int xs = __shfl_up_sync(0xffffffffu, x, d), ys = __shfl_up_sync(0xffffffffu, y, d);
+            if (lane >= d) {
+                x += xs;
+                y += ys;
+            }
         }
-        if (a < v.L) v.goff[a + 1] = run + x;
-        run += __shfl_sync(0xffffffffu, x, 31);
+        if (a < v.L) {
+            v.goff[a + 1] = rows + x;
+            v.toff[a + 1] = tiles + y;
+        }
+        rows += __shfl_sync(0xffffffffu, x, 31);
+        tiles += __shfl_sync(0xffffffffu, y, 31);
     }
-    if (lane == 0) v.goff[0] = 0;
+    if (lane == 0) {
+        v.goff[0] = 0;
+        v.toff[0] = 0;
+        *v.ntile = tiles;
+    }
 }
 
 // Rows into adapter order: one CTA per unit, a warp per entry in turn, each lane
@@ -121,6 +135,21 @@ __global__ void __launch_bounds__(kUnit) plan_order_kernel(PlanView v) {
     }
 }
 
+// The row tiles, a thread each: its adapter by bisection of the tile offsets.
+__global__ void __launch_bounds__(128) plan_tiles_kernel(PlanView v) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
+    if (i >= *v.ntile) return;
+    int lo = 0, hi = v.L - 1;  // the last adapter whose first tile is not past i
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (v.toff[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    const int at = v.goff[lo] + static_cast<int>(i - v.toff[lo]) * kTileRows;
+    const int n = min(kTileRows, v.goff[lo + 1] - at);
+    const int first = v.order[at];
+    v.tile[i] = make_int4(lo, at, n, v.order[at + n - 1] - first == n - 1 ? first : -1);
+}
+
 }  // namespace
 
 int lora_plan_launch(const int32_t* ids, const PlanView& v, int32_t* status, cudaStream_t st) {
@@ -129,6 +158,7 @@ int lora_plan_launch(const int32_t* ids, const PlanView& v, int32_t* status, cud
     plan_groups_kernel<<<static_cast<unsigned>((v.L + 3) / 4), 128, 0, st>>>(v);
     plan_scan_kernel<<<1, 32, 0, st>>>(v);
     plan_order_kernel<<<static_cast<unsigned>(v.units), kUnit, 0, st>>>(v);
+    plan_tiles_kernel<<<static_cast<unsigned>((v.max_tiles + 127) / 128), 128, 0, st>>>(v);
     return launch_result();
 }
 

@@ -1,0 +1,316 @@
+// lora_shrink.cu -- the low-rank products of the adapters:
+//   U[t] = scale[a] X[t] A[a]^T   (forward; A [L, r, K] read along K)
+//   V[t] = scale[a] dY[t] B[a]    (backward; B [L, N, r] read along r)
+//
+// Bound by reading X (dY) once.  A tile is up to 128 rows of one adapter in the
+// plan's order, so nothing is computed for another adapter: neighbouring rows (a
+// sequence's) come by TMA, scattered ones are gathered row by row with cp.async.
+// Rank r leaves few output columns, so the reduction is split over a cluster; each
+// CTA accumulates its share in tensor memory, and after a cluster barrier every
+// CTA sums its part of the tile over the cluster's CTAs in rank order: one
+// rounding, the same bits on every run, no atomics, no scratch in device memory.
+#include "lora.cuh"
+
+namespace gg {
+namespace {
+
+constexpr int kSM = kTileRows;
+constexpr int kSN = 128;             // rank columns of a tile (larger ranks: several tiles)
+constexpr int kSK = 64;              // reduction block
+constexpr int kSMaxStages = 6;
+constexpr int kSThreads = 192;       // producer, issuer, four gather / epilogue warps
+constexpr int kSRing = 98304;        // two CTAs an SM
+
+struct ShrinkParams {
+    PlanView plan;
+    const uint16_t* X;
+    int Kred, r;
+    int take;          // rank columns of a tile
+    int subs;          // tiles the rank is cut into
+    int chunk;         // columns of an MN-major piece of the adapter (16, 32 or 64)
+    int a_slot;        // bytes of a stage's row slot
+    int stage_bytes, stages;
+    const float* scale;
+    uint16_t* out;
+    uint16_t* out_lo;  // the rounding's remainder, in bf16 (or null)
+    int32_t* status;
+};
+
+struct ShrinkCtl {
+    uint64_t full[kSMaxStages];
+    uint64_t empty[kSMaxStages];
+    uint64_t done;
+    uint32_t tmem_base;
+    int abort_flag;
+    int32_t row[kSM];  // the tile's rows
+};
+
+constexpr int kShrinkSmem = 1024 + kSRing + 1024;
+static_assert(sizeof(ShrinkCtl) <= 1024, "control block");
+static_assert(kSRing >= kSM * (kSN + 4) * 4, "partial sums fit the drained ring");
+
+template <bool B_MN>
+__global__ void __launch_bounds__(kSThreads, 2)
+shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmE, const ShrinkParams p,
+              const int S) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    ShrinkCtl* ctl = reinterpret_cast<ShrinkCtl*>(ring + kSRing);
+    volatile int* abort_flag = &ctl->abort_flag;
+    const int warp = warp_id(), lane = lane_id();
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int64_t item = blockIdx.x / S;
+
+    pdl_launch_dependents();
+    // rows without an adapter get zeros: this CTA's share of the units
+    auto zero_bare_rows = [&]() {
+        for (int64_t u = blockIdx.x; u < p.plan.units; u += gridDim.x) {
+            for (int w = warp; w < kUnitWords; w += kSThreads / 32) {
+                const int64_t t0 = u * kUnit + w * 32;
+                uint32_t bare = ~p.plan.any[u * kUnitWords + w];
+                if (p.plan.T - t0 < 32) bare &= p.plan.T > t0 ? (1u << (p.plan.T - t0)) - 1u : 0u;
+                for (; bare; bare &= bare - 1) {
+                    const int64_t at = (t0 + __ffs(bare) - 1) * p.r;
+                    for (int c = lane * 8; c < p.r; c += 256) {
+                        *reinterpret_cast<uint4*>(p.out + at + c) = make_uint4(0, 0, 0, 0);
+                        if (p.out_lo) *reinterpret_cast<uint4*>(p.out_lo + at + c) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+        }
+    };
+    if (item >= static_cast<int64_t>(*p.plan.ntile) * p.subs) {  // the whole cluster
+        zero_bare_rows();
+        return;
+    }
+    const int4 tile = p.plan.tile[item / p.subs];
+    const int a = tile.x, n = tile.z;
+    const bool gather = tile.w < 0;
+    const int c0 = static_cast<int>(item % p.subs) * p.take;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(&ctl->full[s], gather ? 1 + 128 : 1);
+            mbar_init(&ctl->empty[s], 1);
+        }
+        mbar_init(&ctl->done, 1);
+        ctl->abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmE);
+    }
+    if (warp == 1) {
+        tmem_alloc(&ctl->tmem_base, kSN);
+        tmem_relinquish();
+    }
+    if (threadIdx.x >= 64) {
+        const int i = threadIdx.x - 64;
+        if (i < n) ctl->row[i] = p.plan.order[tile.y + i];
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const int nb = (p.Kred + kSK - 1) / kSK;
+    const int lo = static_cast<int>(static_cast<int64_t>(nb) * rank / S);
+    const int hi = static_cast<int>(static_cast<int64_t>(nb) * (rank + 1) / S);  // at least one block: S <= nb
+    const uint32_t tmem = ctl->tmem_base;
+    const uint32_t ring0 = smem_u32(ring);
+    const int pieces = (p.take + p.chunk - 1) / p.chunk;   // MN-major pieces of the adapter
+    const uint32_t piece_bytes = static_cast<uint32_t>(p.chunk) * kSK * 2;
+
+    if (warp == 0) {
+        // ------------------------------------------------------- producer --
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int issued = 0;
+            const uint32_t ebytes = B_MN ? piece_bytes * pieces : static_cast<uint32_t>(p.take) * 128u;
+            for (int b = lo; b < hi; ++b) {
+                if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) break;
+                uint8_t* sA = ring + stage * p.stage_bytes;
+                uint8_t* sB = sA + p.a_slot;
+                uint64_t* bar = &ctl->full[stage];
+                mbar_arrive_expect_tx(bar, ebytes + (gather ? 0u : static_cast<uint32_t>(p.a_slot)));
+                if (!gather) tma_load_2d(sA, &tmX, bar, b * kSK, tile.w);
+                if (B_MN) {
+                    for (int c = 0; c < pieces; ++c)
+                        tma_load_3d(sB + c * piece_bytes, &tmE, bar, c0 + c * p.chunk, b * kSK, a);
+                } else {
+                    tma_load_3d(sB, &tmE, bar, b * kSK, c0, a);
+                }
+                ++issued;
+                if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+            }
+            // every copy has landed before the ring is reused or the CTA exits
+            for (int j = 0; j < min(issued, p.stages); ++j) {
+                if (--stage < 0) { stage = p.stages - 1; phase ^= 1u; }
+                int dummy = 0;
+                mbar_wait(&ctl->full[stage], phase, reinterpret_cast<volatile int*>(&dummy), p.status);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ----------------------------------------------------- MMA issuer --
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool any_mma = false;
+            const int cols = B_MN ? pieces * p.chunk : (p.take + 15) / 16 * 16;
+            const uint32_t idesc = idesc_bf16_f32_n(kSM, cols, 0, B_MN ? 1 : 0);
+            for (int b = lo; b < hi; ++b) {
+                if (!mbar_wait(&ctl->full[stage], phase, abort_flag, p.status)) break;
+                tc_fence_after();
+                if (gather) fence_proxy_async_smem();  // gathered rows are generic-proxy writes
+                const uint32_t sA = ring0 + stage * p.stage_bytes, sB = sA + p.a_slot;
+#pragma unroll
+                for (int ks = 0; ks < kSK / 16; ++ks) {
+                    const uint64_t ad = smem_desc(sA + ks * 32, 16, 1024, kLayoutSw128);
+                    const uint64_t bd = B_MN ? mnmajor_desc(sB + ks * 32 * p.chunk, 2 * p.chunk, piece_bytes)
+                                             : smem_desc(sB + ks * 32, 16, 1024, kLayoutSw128);
+                    umma_bf16(tmem, ad, bd, idesc, (b > lo || ks > 0) ? 1u : 0u);
+                }
+                umma_commit(&ctl->empty[stage]);
+                any_mma = true;
+                if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+            }
+            if (any_mma) umma_commit(&ctl->done);
+            else mbar_arrive(&ctl->done);
+        }
+        __syncwarp();
+    } else if (gather) {
+        // ---------------------------------------------------- row gathers --
+        // thread: 16-byte piece gt & 7 of rows gt / 8 + 16 j; rows past the tile's
+        // end are left as they are (their accumulator rows are not stored)
+        const int gt = threadIdx.x - 64;
+        const int pc = gt & 7;
+        const uint16_t* src[kSM / 16];
+#pragma unroll
+        for (int j = 0; j < kSM / 16; ++j) {
+            const int rr = (gt >> 3) + 16 * j;
+            src[j] = rr < n ? p.X + static_cast<int64_t>(ctl->row[rr]) * p.Kred + pc * 8 : nullptr;
+        }
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int b = lo; b < hi; ++b) {
+            if (!warp_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status, 32)) break;
+            const uint32_t sA = ring0 + stage * p.stage_bytes;
+            const bool in = b * kSK + pc * 8 < p.Kred;
+#pragma unroll
+            for (int j = 0; j < kSM / 16; ++j) {
+                const int rr = (gt >> 3) + 16 * j;
+                if (rr < n)
+                    cp_async_16(sA + rr * 128 + ((pc ^ (rr & 7)) << 4), in ? src[j] + b * kSK : p.X, in ? 16u : 0u);
+            }
+            cp_async_mbar_arrive(&ctl->full[stage]);
+            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+        }
+        cp_async_wait<0>();
+    }
+
+    // -------------------------------------------- partial sums to the cluster --
+    const bool good = warp_wait(&ctl->done, 0, abort_flag, p.status);
+    tc_fence_after();
+    __syncthreads();  // the copies have landed, the MMAs have completed: the ring is free
+    float* part = reinterpret_cast<float*>(ring);
+    const int groups = min(p.take, p.r - c0) / 8;
+    const int pitch = p.take + 4;
+    const int q = warp & 3;
+    if (warp >= 2 && q * 32 < n) {
+        for (int c = 0; c < 8 * groups; c += 8) {
+            uint32_t v[8];
+            tmem_ld_32x32b_x8(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, v);
+            tmem_ld_wait();
+            float* d = part + (q * 32 + lane) * pitch + c;
+            *reinterpret_cast<uint4*>(d) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(d + 4) = make_uint4(v[4], v[5], v[6], v[7]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (good) {
+        const float sc = p.scale ? p.scale[a] : 1.0f;
+        for (int i = rank * kSThreads + threadIdx.x; i < n * groups; i += S * kSThreads) {
+            const int rr = i / groups, c = (i % groups) * 8;
+            float s[8], rest[8];
+            cluster_sum8(smem_u32(part + rr * pitch + c), S, s);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                s[k] *= sc;
+                const float h = __bfloat162float(__float2bfloat16(s[k]));
+                rest[k] = fabsf(h) < __int_as_float(0x7f800000) ? s[k] - h : 0.f;
+            }
+            // U (V) is an operand of the tensor cores: bf16, and for the adapter
+            // gradients, which sum it over tokens, its remainder as a second bf16
+            const int64_t at = static_cast<int64_t>(ctl->row[rr]) * p.r + c0 + c;
+            *reinterpret_cast<uint4*>(p.out + at) = pack_bf16x8(s);
+            if (p.out_lo) *reinterpret_cast<uint4*>(p.out_lo + at) = pack_bf16x8(rest);
+        }
+    }
+    zero_bare_rows();
+    __syncthreads();
+    cluster_sync();  // no CTA leaves while another may still read its sums
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kSN);
+    }
+}
+
+template <bool B_MN>
+int launch_shrink(const CUtensorMap& x, const CUtensorMap& e, const ShrinkParams& p, cudaStream_t st) {
+    static ClusterRoom rooms;
+    const int* room = nullptr;
+    int rc = rooms.get(shrink_kernel<B_MN>, kSThreads, kShrinkSmem, &room);
+    if (rc != GG_OK) return rc;
+    // The split: as many CTAs as are resident at once for the tiles a batch of
+    // sequences has (whole tiles and half of the adapters' ragged ones).
+    const int64_t nb = (p.Kred + kSK - 1) / kSK;
+    const int64_t ragged = p.plan.max_tiles - p.plan.T / kTileRows;
+    const int64_t tiles = (p.plan.T / kTileRows + (ragged + 1) / 2) * p.subs;
+    int S = kMaxCluster;
+    while (S > 1 && (tiles > room[S] || S > nb)) --S;
+    const int64_t grid = p.plan.max_tiles * p.subs * S;
+    if (grid >= (int64_t(1) << 31)) return GG_ERR_UNSUPPORTED;
+    ClusterLaunch l(grid, kSThreads, kShrinkSmem, S, false, st);
+    clear_pending_launch_error();
+    const cudaError_t err = cudaLaunchKernelEx(&l.cfg, shrink_kernel<B_MN>, x, e, p, S);
+    if (err != cudaSuccess) { record_cuda_error(err); return GG_ERR_CUDA; }
+    return launch_result();
+}
+
+}  // namespace
+
+int lora_shrink_launch(bool b_mn, const uint16_t* X, const uint16_t* ad, const float* scale, const PlanView& plan,
+                       int64_t Kred, int r, uint16_t* out, uint16_t* out_lo, int32_t* status, cudaStream_t st) {
+    ShrinkParams p{};
+    p.plan = plan;
+    p.X = X;
+    p.Kred = static_cast<int>(Kred);
+    p.r = r;
+    p.take = r < kSN ? r : kSN;
+    p.subs = (r + kSN - 1) / kSN;
+    p.chunk = rank_pad(p.take);
+    p.scale = scale;
+    p.out = out;
+    p.out_lo = out_lo;
+    p.status = status;
+    const int rows = plan.T >= kSM ? kSM : static_cast<int>((plan.T + 7) / 8 * 8);
+    p.a_slot = rows * 128;
+    // adapter slot: rank rows of 128 bytes, or MN-major pieces of kSK rows; at least
+    // what the MMA reads past it of the row slot stays inside the ring
+    const int e = b_mn ? (p.take + p.chunk - 1) / p.chunk * p.chunk * kSK * 2 : (p.take + 15) / 16 * 16 * 128;
+    p.stage_bytes = (p.a_slot + e + 1023) / 1024 * 1024;
+    p.stages = (kSRing - kSM * 128) / p.stage_bytes;
+    if (p.stages > kSMaxStages) p.stages = kSMaxStages;
+    CUtensorMap mX{}, mE{};
+    if (!encode_map_2d(&mX, X, Kred, plan.T, Kred, kSK, rows)) return GG_ERR_CUDA;
+    if (b_mn) {
+        if (!encode_map_3d(&mE, ad, r, Kred, plan.L, r, Kred * r, p.chunk, kSK)) return GG_ERR_CUDA;
+        return launch_shrink<true>(mX, mE, p, st);
+    }
+    if (!encode_map_3d(&mE, ad, Kred, r, plan.L, Kred, Kred * r, kSK, p.take)) return GG_ERR_CUDA;
+    return launch_shrink<false>(mX, mE, p, st);
+}
+
+}  // namespace gg
