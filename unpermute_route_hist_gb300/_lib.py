@@ -108,6 +108,8 @@ class GGError(RuntimeError):
 
 def load() -> ctypes.CDLL:
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

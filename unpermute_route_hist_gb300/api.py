@@ -19,7 +19,8 @@ def _p(t):
 
 
 def _stream(device=None):
-    return torch.cuda.current_stream(device).cuda_stream
+    """The device's current stream as a handle (without building a torch.cuda.Stream)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device.index)
 
 
 def _need(t, dtype, name, shape=None):
@@ -322,6 +323,7 @@ def dual_asym(X0, X1, W0, W1, trans_a=False, trans_b=False, *, out0=None, out1=N
 class LoraPlan:
     """A batch's adapter ids, read once: which adapters occur among which rows, and
     the rows sorted by adapter.  Serves every projection and layer of the batch."""
+    __slots__ = ("buf", "T", "L")
 
     def __init__(self, buf, T: int, L: int):
         self.buf, self.T, self.L = buf, T, L
@@ -332,9 +334,8 @@ def lora_plan(ids, L: int, *, out=None, status=None) -> LoraPlan:
     buffer of at least lora_plan_size(T, L) bytes."""
     _need(ids, torch.int32, "ids", (ids.shape[0],))
     T = ids.shape[0]
-    nbytes = lora_plan_size(T, L)
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=ids.device)
+        out = torch.empty(lora_plan_size(T, L), dtype=torch.uint8, device=ids.device)
     elif not out.is_cuda or not out.is_contiguous():
         raise ValueError("out must be a contiguous CUDA tensor")
     rc = _lib.load().gg_lora_plan(_p(ids), T, L, _p(out), _nbytes(out), _p(status), _stream(ids.device))
@@ -350,30 +351,45 @@ def lora_backward_workspace_size(T: int, r: int) -> int:
     return int(_lib.load().gg_lora_backward_workspace_size(T, r))
 
 
-def _lora_shapes(X, A, scale, plan):
-    _need(X, torch.bfloat16, "X")
+def _all_bf16(tensors, shapes):
+    """Whether every tensor is a contiguous bf16 CUDA tensor of its shape (the calls'
+    quick check; the slower _need then says what is wrong)."""
+    for t, shape in zip(tensors, shapes):
+        if t.dtype is not torch.bfloat16 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+            return False
+    return True
+
+
+def _lora_sizes(X, W, A, B, scale, plan):
+    """(T, K, L, r, N) of the operands, checked."""
     T, K = X.shape
     L, r, _ = A.shape
-    _need(A, torch.bfloat16, "A", (L, r, K))
-    _opt(scale, torch.float32, "scale", (L,))
+    N = W.shape[0]
+    shapes = ((T, K), (N, K), (L, r, K), (L, N, r))
+    if not _all_bf16((X, W, A, B), shapes):
+        for t, name, shape in zip((X, W, A, B), "XWAB", shapes):
+            _need(t, torch.bfloat16, name, shape)
+    if scale is not None and (scale.dtype is not torch.float32 or scale.shape != (L,) or not scale.is_cuda
+                              or not scale.is_contiguous()):
+        _need(scale, torch.float32, "scale", (L,))
     if plan.T != T or plan.L != L:
         raise ValueError("plan is of %d tokens and %d adapters, the call of %d and %d" % (plan.T, plan.L, T, L))
-    return T, K, L, r
+    return T, K, L, r, N
 
 
 def lora_forward(X, W, A, B, scale, plan: LoraPlan, *, out=None, out_u=None, status=None):
     """(Y [T, N], U [T, r]): X W^T + U B[a]^T with U = scale[a] X A[a]^T, a the token's
     adapter in plan.  X [T, K], W [N, K], A [L, r, K], B [L, N, r]; scale [L] fp32 or
     None.  U is what lora_backward needs of the forward."""
-    T, K, L, r = _lora_shapes(X, A, scale, plan)
-    N = W.shape[0]
-    _need(W, torch.bfloat16, "W", (N, K))
-    _need(B, torch.bfloat16, "B", (L, N, r))
-    Y = _out(out, (T, N), torch.bfloat16, X.device, "out")
-    U = _out(out_u, (T, r), torch.bfloat16, X.device, "out_u")
-    rc = _lib.load().gg_lora_forward(_p(X), _p(W), _p(A), _p(B), _p(scale), _p(plan.buf), T, L, r, N, K, _p(Y), _p(U),
-                                     _p(status), _stream(X.device))
-    _lib.check("gg_lora_forward", rc)
+    T, K, L, r, N = _lora_sizes(X, W, A, B, scale, plan)
+    dev = X.device
+    Y = _out(out, (T, N), torch.bfloat16, dev, "out")
+    U = _out(out_u, (T, r), torch.bfloat16, dev, "out_u")
+    rc = _lib.load().gg_lora_forward(X.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(), _p(scale),
+                                     plan.buf.data_ptr(), T, L, r, N, K, Y.data_ptr(), U.data_ptr(), _p(status),
+                                     _stream(dev))
+    if rc:
+        _lib.check("gg_lora_forward", rc)
     return Y, U
 
 
@@ -382,20 +398,20 @@ def lora_backward(dY, X, W, A, B, scale, plan: LoraPlan, U, *, want=(True, True,
     """(dX [T, K], dA [L, r, K], dB [L, N, r]): the gradient of lora_forward (W is frozen);
     want selects them (None in the place of the others).  workspace: a tensor of
     lora_backward_workspace_size(T, r) bytes, allocated here by default."""
-    T, K, L, r = _lora_shapes(X, A, scale, plan)
-    N = W.shape[0]
-    _need(W, torch.bfloat16, "W", (N, K))
-    _need(B, torch.bfloat16, "B", (L, N, r))
-    _need(dY, torch.bfloat16, "dY", (T, N))
-    _need(U, torch.bfloat16, "U", (T, r))
+    T, K, L, r, N = _lora_sizes(X, W, A, B, scale, plan)
+    if not _all_bf16((dY, U), ((T, N), (T, r))):
+        _need(dY, torch.bfloat16, "dY", (T, N))
+        _need(U, torch.bfloat16, "U", (T, r))
     dev = dY.device
     dX = _out(out, (T, K), torch.bfloat16, dev, "out") if want[0] else None
     dA = _out(out_da, (L, r, K), torch.bfloat16, dev, "out_da") if want[1] else None
     dB = _out(out_db, (L, N, r), torch.bfloat16, dev, "out_db") if want[2] else None
     ws = _workspace(workspace, lora_backward_workspace_size(T, r) if want[0] or want[1] else 0, dev)
-    rc = _lib.load().gg_lora_backward(_p(dY), _p(X), _p(W), _p(A), _p(B), _p(scale), _p(plan.buf), _p(U), T, L, r, N,
-                                      K, _p(dX), _p(dA), _p(dB), _p(ws), _nbytes(ws), _p(status), _stream(dev))
-    _lib.check("gg_lora_backward", rc)
+    rc = _lib.load().gg_lora_backward(dY.data_ptr(), X.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(), _p(scale),
+                                      plan.buf.data_ptr(), U.data_ptr(), T, L, r, N, K, _p(dX), _p(dA), _p(dB),
+                                      _p(ws), _nbytes(ws), _p(status), _stream(dev))
+    if rc:
+        _lib.check("gg_lora_backward", rc)
     return dX, dA, dB
 
 
@@ -403,49 +419,54 @@ _ROPE_DTYPES = {torch.bfloat16: _lib.GG_DTYPE_BF16, torch.float16: _lib.GG_DTYPE
                 torch.float32: _lib.GG_DTYPE_F32}
 
 
-def _rope_heads(x, like, name):
-    """[T, H, D] with D contiguous (any token and head strides) of `like`'s type and device."""
-    if not x.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if x.dim() != 3 or x.dtype != like.dtype or x.shape[0] != like.shape[0] or x.shape[2] != like.shape[2]:
-        raise ValueError("%s must be [%d, heads, %d] of %s, got %s of %s"
-                         % (name, like.shape[0], like.shape[2], like.dtype, tuple(x.shape), x.dtype))
-    if x.shape[2] > 1 and x.stride(2) != 1:
+def _rope_heads(x, shape, dtype, name):
+    """(token stride, head stride) of heads [T, H, D] with D contiguous."""
+    if x.dtype is not dtype or not x.is_cuda or x.shape != shape:
+        raise ValueError("%s must be a CUDA tensor %s of %s, got %s of %s"
+                         % (name, tuple(shape), dtype, tuple(x.shape), x.dtype))
+    tok, head, one = x.stride()
+    if one != 1 and shape[2] > 1:
         raise ValueError("%s: the elements of a head must be contiguous" % name)
-    return x
-
-
-def _rope_out(out, x, name):
-    if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if out.shape != x.shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(out.shape), tuple(x.shape)))
-    return _rope_heads(out, x, name)
+    return tok, head
 
 
 def _rope(q, k, positions, freqs, interleaved, out_q, out_k, backward):
-    import ctypes
-    if q.dtype not in _ROPE_DTYPES:
-        raise TypeError("q must be bfloat16, float16 or float32, got %s" % q.dtype)
-    _rope_heads(q, q, "q")
-    T, n_q, D = q.shape
-    rot = freqs.rot_dim
+    dtype, shape = q.dtype, q.shape
+    code = _ROPE_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError("q must be bfloat16, float16 or float32, got %s" % dtype)
+    T, n_q, D = shape
+    dev = q.device
+    rot, axes = freqs.rot_dim, freqs.axes
     if rot > D:
         raise ValueError("freqs turn %d elements of a head of %d" % (rot, D))
-    axes = 1 if freqs.sections is None else len(freqs.sections)
-    _need(positions, torch.int32, "positions", (T,) if axes == 1 and positions.dim() == 1 else (axes, T))
-    oq = _rope_out(out_q, q, "out_q")
-    n_k, ok, ks, oks = 0, None, (0, 0), (0, 0)
-    if k is not None:
-        _rope_heads(k, q, "k")
-        ok = _rope_out(out_k, k, "out_k")
-        n_k, ks, oks = k.shape[1], (k.stride(0), k.stride(1)), (ok.stride(0), ok.stride(1))
-    sec = (ctypes.c_int32 * axes)(*freqs.sections) if axes > 1 else None
-    rc = _lib.load().gg_rope(_p(q), q.stride(0), q.stride(1), n_q, _p(k), ks[0], ks[1], n_k, _p(oq), oq.stride(0),
-                             oq.stride(1), _p(ok), oks[0], oks[1], _p(positions), axes, sec, _p(freqs.steps),
-                             freqs.attention_scale, T, D, rot, int(interleaved), _ROPE_DTYPES[q.dtype], int(backward),
-                             _stream(q.device))
-    _lib.check("gg_rope", rc)
+    want = (T,) if axes == 1 and positions.dim() == 1 else (axes, T)
+    if positions.dtype is not torch.int32 or positions.shape != want or not positions.is_cuda or \
+            not positions.is_contiguous():
+        _need(positions, torch.int32, "positions", want)
+    qt, qh = _rope_heads(q, shape, dtype, "q")
+    if out_q is q:
+        oq, ot, oh = q, qt, qh
+    else:
+        oq = torch.empty(shape, dtype=dtype, device=dev) if out_q is None else out_q
+        ot, oh = _rope_heads(oq, shape, dtype, "out_q")
+    if k is None:
+        n_k, kp, okp, kt, kh, okt, okh, ok = 0, None, None, 0, 0, 0, 0, None
+    else:
+        n_k = k.shape[1]
+        kshape = (T, n_k, D)
+        kt, kh = _rope_heads(k, kshape, dtype, "k")
+        if out_k is k:
+            ok, okt, okh = k, kt, kh
+        else:
+            ok = torch.empty(kshape, dtype=dtype, device=dev) if out_k is None else out_k
+            okt, okh = _rope_heads(ok, kshape, dtype, "out_k")
+        kp, okp = k.data_ptr(), ok.data_ptr()
+    rc = _lib.load().gg_rope(q.data_ptr(), qt, qh, n_q, kp, kt, kh, n_k, oq.data_ptr(), ot, oh, okp, okt, okh,
+                             positions.data_ptr(), axes, freqs.c_sections, freqs.steps.data_ptr(),
+                             freqs.attention_scale, T, D, rot, interleaved, code, backward, _stream(dev))
+    if rc:
+        _lib.check("gg_rope", rc)
     return oq, ok
 
 
@@ -454,9 +475,9 @@ def rope(q, k, positions, freqs, *, interleaved=False, out_q=None, out_k=None):
     views of a packed projection.  positions [T] int32, or [axes, T] with sections; freqs from
     rope_freqs; interleaved pairs elements (2i, 2i+1), else (i, i + rot/2).  out_q=q, out_k=k
     turns them in place."""
-    return _rope(q, k, positions, freqs, interleaved, out_q, out_k, False)
+    return _rope(q, k, positions, freqs, interleaved, out_q, out_k, 0)
 
 
 def rope_bwd(dq, dk, positions, freqs, *, interleaved=False, out_q=None, out_k=None):
     """(dq, dk) of rope's inputs from the gradients of its outputs; arguments as rope's."""
-    return _rope(dq, dk, positions, freqs, interleaved, out_q, out_k, True)
+    return _rope(dq, dk, positions, freqs, interleaved, out_q, out_k, 1)

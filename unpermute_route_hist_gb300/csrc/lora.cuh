@@ -165,32 +165,28 @@ __device__ __forceinline__ void pdl_wait() {
     asm volatile("fence.proxy.async;" ::: "memory");  // its stores, before this thread's TMA reads of them
 }
 
-// The sum of eight floats at the same shared-memory offset in CTAs 0 .. n-1 of
-// the cluster (at most 8), in that order; all reads are in flight together.
-__device__ __forceinline__ void cluster_sum8(uint32_t addr, int n, float (&s)[8]) {
-    float4 x[8], y[8];
+// The sum of four floats at the same shared-memory offset in CTAs 0 .. n-1 of the
+// cluster (at most 8), in that order; all reads are in flight together.
+__device__ __forceinline__ float4 cluster_sum4(uint32_t addr, int n) {
+    float4 x[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        if (c < n) x[c] = ld_cluster_f32x4(mapa_addr(addr, static_cast<uint32_t>(c)));
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
         if (c < n) {
-            const uint32_t a = mapa_addr(addr, static_cast<uint32_t>(c));
-            x[c] = ld_cluster_f32x4(a);
-            y[c] = ld_cluster_f32x4(a + 16);
+            s.x += x[c].x;
+            s.y += x[c].y;
+            s.z += x[c].z;
+            s.w += x[c].w;
         }
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) s[q] = 0.f;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        if (c < n) {
-            s[0] += x[c].x; s[1] += x[c].y; s[2] += x[c].z; s[3] += x[c].w;
-            s[4] += y[c].x; s[5] += y[c].y; s[6] += y[c].z; s[7] += y[c].w;
-        }
-    }
+    return s;
 }
 
-__device__ __forceinline__ uint4 pack_bf16x8(const float (&s)[8]) {
-    return make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]),
-                      pack_bf16x2(s[6], s[7]));
+__device__ __forceinline__ uint2 pack_bf16x4(const float4& s) {
+    return make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
 }
 
 // ------------------------------------------------------------------ host --
@@ -225,34 +221,37 @@ struct ClusterLaunch {
 
 constexpr int kMaxCluster = 8;
 
-// Per kernel: the shared-memory opt-in and how many clusters of 1 .. 8 CTAs are
-// resident at once with smem bytes, asked once per device.  GG_OK or an error code.
+// An empty kernel of the same block shape: the occupancy query answers one CTA an SM
+// for every kernel that allocates tensor memory, although two are resident at once
+// (measured: 304 CTAs of 100 KB, each with 128 TMEM columns, ran together).
+static __global__ void __launch_bounds__(192, 2) cluster_room_kernel() {}
+
+// Per kernel: the shared-memory opt-in and how many clusters of 1 .. 8 CTAs of 192
+// threads are resident at once with smem bytes, asked once per device.  GG_OK or an
+// error code.
 struct ClusterRoom {
     std::atomic<int> n[64][kMaxCluster + 1];  // 0: not asked yet
     template <typename K>
-    int get(K kern, int threads, size_t smem, const int** room) {
+    int get(K kern, size_t smem, int (&room)[kMaxCluster + 1]) {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) { record_cuda_error(e); return GG_ERR_CUDA; }
         if (dev < 0 || dev >= 64) dev = 0;
-        static thread_local int out[kMaxCluster + 1];
         if (n[dev][kMaxCluster].load(std::memory_order_acquire) == 0) {
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            const int bytes = static_cast<int>(smem);
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(cluster_room_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
             for (int S = 1; S <= kMaxCluster && e == cudaSuccess; ++S) {
-                ClusterLaunch l(int64_t(S) * 1024, threads, smem, S, false, nullptr);
+                ClusterLaunch l(int64_t(S) * 1024, 192, smem, S, false, nullptr);
                 int c = 0;
-                e = cudaOccupancyMaxActiveClusters(&c, kern, &l.cfg);
+                e = cudaOccupancyMaxActiveClusters(&c, cluster_room_kernel, &l.cfg);
                 if (e == cudaSuccess && c < 1) e = cudaErrorInvalidConfiguration;
-                n[dev][S].store(c, std::memory_order_release);
+                if (e == cudaSuccess) n[dev][S].store(c, std::memory_order_release);
             }
-            if (e != cudaSuccess) {
-                n[dev][kMaxCluster].store(0, std::memory_order_release);
-                record_cuda_error(e);
-                return GG_ERR_CUDA;
-            }
+            if (e != cudaSuccess) { record_cuda_error(e); return GG_ERR_CUDA; }
         }
-        for (int S = 1; S <= kMaxCluster; ++S) out[S] = n[dev][S].load(std::memory_order_acquire);
-        *room = out;
+        for (int S = 1; S <= kMaxCluster; ++S) room[S] = n[dev][S].load(std::memory_order_acquire);
         return GG_OK;
     }
 };

@@ -22,7 +22,8 @@ constexpr int kGK = 64;             // rows of a block
 constexpr int kGThreads = 192;      // producer, issuer, four gather / epilogue warps
 constexpr int kGWide = kGM * kGK * 2;
 constexpr int kGMaxStages = 6;
-// the partial sums (rank up to 64: two CTAs an SM) fit the drained ring
+// the partial sums fit the drained ring
+static_assert(73728 >= 4 * kGM * (32 + 4) && 73728 >= 4 * 32 * (kGM + 4), "ring");
 static_assert(98304 >= 4 * kGM * (64 + 4) && 98304 >= 4 * 64 * (kGM + 4), "ring");
 static_assert(196608 >= 4 * kGM * (kLoraMaxRank + 4) && 196608 >= 4 * kLoraMaxRank * (kGM + 4), "ring");
 
@@ -58,9 +59,9 @@ struct GradMaps {
     CUtensorMap narrow[3];     // V, V's remainder, U
 };
 
-// RING: bytes of the operand ring (two CTAs an SM, or one)
-template <int RING>
-__global__ void __launch_bounds__(kGThreads, RING > 98304 ? 1 : 2)
+// RING: bytes of the operand ring; CTAS: resident on an SM
+template <int RING, int CTAS>
+__global__ void __launch_bounds__(kGThreads, CTAS)
 grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int S) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -264,22 +265,18 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int
     if (good) {
         const int wide = min(kGM, side.cols - col0);
         if (sd == 0) {
-            const int groups = wide / 8;
-            for (int i = rank * kGThreads + threadIdx.x; i < p.r * groups; i += S * kGThreads) {
-                const int c = i / groups, k = (i % groups) * 8;
-                float s[8];
-                cluster_sum8(smem_u32(part + c * pitch + k), act, s);
-                *reinterpret_cast<uint4*>(side.out + (static_cast<int64_t>(a) * p.r + c) * side.cols + col0 + k) =
-                    pack_bf16x8(s);
+            const int quads = wide / 4;
+            for (int i = rank * kGThreads + threadIdx.x; i < p.r * quads; i += S * kGThreads) {
+                const int c = i / quads, k = (i % quads) * 4;
+                *reinterpret_cast<uint2*>(side.out + (static_cast<int64_t>(a) * p.r + c) * side.cols + col0 + k) =
+                    pack_bf16x4(cluster_sum4(smem_u32(part + c * pitch + k), act));
             }
         } else {
-            const int groups = p.r / 8;
-            for (int i = rank * kGThreads + threadIdx.x; i < wide * groups; i += S * kGThreads) {
-                const int n = i / groups, c = (i % groups) * 8;
-                float s[8];
-                cluster_sum8(smem_u32(part + n * pitch + c), act, s);
-                *reinterpret_cast<uint4*>(side.out + (static_cast<int64_t>(a) * side.cols + col0 + n) * p.r + c) =
-                    pack_bf16x8(s);
+            const int quads = p.r / 4;
+            for (int i = rank * kGThreads + threadIdx.x; i < wide * quads; i += S * kGThreads) {
+                const int n = i / quads, c = (i % quads) * 4;
+                *reinterpret_cast<uint2*>(side.out + (static_cast<int64_t>(a) * side.cols + col0 + n) * p.r + c) =
+                    pack_bf16x4(cluster_sum4(smem_u32(part + n * pitch + c), act));
             }
         }
     }
@@ -291,12 +288,12 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int
     }
 }
 
-template <int RING>
+template <int RING, int CTAS>
 int launch_grad(const GradMaps& m, GradParams p, cudaStream_t st) {
     constexpr size_t smem = 1024 + RING;
     static ClusterRoom rooms;
-    const int* room = nullptr;
-    const int rc = rooms.get(grad_kernel<RING>, kGThreads, smem, &room);
+    int room[kMaxCluster + 1];
+    const int rc = rooms.get(grad_kernel<RING, CTAS>, smem, room);
     if (rc != GG_OK) return rc;
     p.stages = RING / p.stage_bytes;
     if (p.stages > kGMaxStages) p.stages = kGMaxStages;
@@ -309,7 +306,7 @@ int launch_grad(const GradMaps& m, GradParams p, cudaStream_t st) {
     if (items * S >= (int64_t(1) << 31)) return GG_ERR_UNSUPPORTED;
     ClusterLaunch l(items * S, kGThreads, smem, S, false, st);
     clear_pending_launch_error();
-    const cudaError_t err = cudaLaunchKernelEx(&l.cfg, grad_kernel<RING>, m, p, S);
+    const cudaError_t err = cudaLaunchKernelEx(&l.cfg, grad_kernel<RING, CTAS>, m, p, S);
     if (err != cudaSuccess) { record_cuda_error(err); return GG_ERR_CUDA; }
     return launch_result();
 }
@@ -340,8 +337,10 @@ int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, c
         if (!encode_map_2d(&m.wide[1], dY, N, plan.T, N, 64, kGK)) return GG_ERR_CUDA;
         if (!encode_map_2d(&m.narrow[2], U, r, plan.T, r, p.chunk, kGK)) return GG_ERR_CUDA;
     }
-    // two CTAs an SM for ranks up to 64, one above
-    return p.nc == 1 ? launch_grad<98304>(m, p, st) : launch_grad<196608>(m, p, st);
+    // rings of at least three stages while two CTAs fit an SM (ranks up to 64), three
+    // CTAs for ranks up to 32
+    if (p.chunk <= 32) return launch_grad<73728, 3>(m, p, st);
+    return p.nc == 1 ? launch_grad<98304, 2>(m, p, st) : launch_grad<196608, 1>(m, p, st);
 }
 
 }  // namespace gg

@@ -1,6 +1,6 @@
 // lora_pair.cu -- the shared projection with its adapters for batches of many
 // rows: Y = X W^T + U B[a]^T and dX = dY W + V A[a], persistent 2-CTA tiles of
-// 256 rows and up to 256 columns (cta_group::2 tcgen05 MMAs, accumulators double-buffered in tensor
+// 256 x 256 (cta_group::2 tcgen05 MMAs, accumulators double-buffered in tensor
 // memory, TMA-fed six-stage ring).
 //
 // Rows stay in token order: the shared product is one dense GEMM, bound by the
@@ -29,7 +29,6 @@ constexpr int kPGroup = 8;             // 256-row units of a raster group
 struct PairParams {
     PlanView plan;
     int Kred, ncols, r, rpad, epb;
-    int width;         // columns of a tile: 256, 224 or 192
     int ntiles;        // column tiles
     int64_t tiles;     // all of them
     uint16_t* out;
@@ -60,7 +59,7 @@ __device__ __forceinline__ PairTile pair_tile(int64_t t, const PairParams& p) {
     const int64_t left = p.plan.units - first;
     const int h = static_cast<int>(left < kPGroup ? left : kPGroup);
     const int loc = static_cast<int>(t - group * per);
-    return {first + loc % h, (loc / h) * p.width};
+    return {first + loc % h, (loc / h) * kPN};
 }
 
 template <bool B_MN>
@@ -116,15 +115,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             uint32_t phase = 0;
             int64_t issued = 0;
             bool ok = true, waited = false;
-            // bytes of a stage in one CTA: its rows, and its half of the columns (read
-            // along them: whole 64-column pieces)
-            const uint32_t base_bytes = kPSlot + (B_MN ? kPSlot : static_cast<uint32_t>(p.width) * kPK);
-            const uint32_t eb = 256u * p.rpad;  // slot of an adapter's columns
-            const uint32_t ebytes = B_MN ? eb : static_cast<uint32_t>(p.width) * p.rpad;
+            const uint32_t eb = 256u * p.rpad;  // bytes of an adapter's columns, and of the rows' U
             for (int64_t t = slot; t < p.tiles && ok; t += nslot) {
                 const PairTile ti = pair_tile(t, p);
                 const int32_t arow = static_cast<int32_t>(ti.unit * kUnit + rank * kPM);
-                const int32_t nh = ti.n0 + static_cast<int32_t>(rank) * (p.width / 2);
+                const int32_t nh = ti.n0 + static_cast<int32_t>(rank) * (kPN / 2);
                 const int ne = p.plan.cnt[ti.unit];
                 const int32_t* gid = p.plan.gid + ti.unit * p.plan.slots;
                 const int total = nb + ext_blocks(ne);
@@ -135,7 +130,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                     const uint32_t bar = mapa_u32(&ctl->full[stage], 0);
                     if (i < nb) {
                         const int32_t red = i * kPK;
-                        if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2 * base_bytes);
+                        if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2 * kPStage);
                         tma_load_2d_pair(sA, &tmX, bar, red, arow);
                         if (B_MN) {
                             tma_load_2d_pair(sB, &tmW, bar, nh, red);
@@ -149,7 +144,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                         const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
                         const int en = p.r <= 64 ? min(p.epb, ne - ef) : 1;
                         const int rc = p.r <= 64 ? 0 : (xi % rchunks) * 64;
-                        if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2u * (eb + ebytes * en));
+                        if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2u * (eb + eb * en));
                         tma_load_2d_pair(sA, &tmU, bar, rc, arow);
                         for (int e = 0; e < en; ++e) {
                             const int g = gid[ef + e];
@@ -179,7 +174,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
     } else if (warp == 1) {
         // ----------------------------------------------------- MMA issuer --
         if (leader && lane == 0) {
-            const uint32_t idesc = idesc_bf16_f32_n(2 * kPM, p.width, 0, B_MN ? 1 : 0);
+            constexpr uint32_t idesc = idesc_bf16_f32(2 * kPM, kPN, 0, B_MN ? 1 : 0);
             int stage = 0;
             uint32_t phase = 0, acc = 0;
             bool ok = true, any_mma = false;
@@ -253,10 +248,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             if (!warp_wait(&ctl->tmem_full[buf], (acc >> 1) & 1u, abort_flag, p.status, 64, true)) break;
             tc_fence_after();
             const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * kPN;
-            const int end = min(p.ncols, ti.n0 + p.width);  // the tile's columns end here
 #pragma unroll 1
             for (int c = 0; c < kPN; c += 128) {
-                // (a narrower tile's last loads read columns nothing was accumulated in)
                 uint32_t v[4][32];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(ta + c + 32 * k, v[k]);
@@ -285,11 +278,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                                               pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
                                               pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
                         }
-                        if (p.st32 && col + 8 < end) {
+                        if (p.st32 && col + 8 < p.ncols) {
                             st_global_32_policy(orow + col, o[0], o[1], pol);
                         } else {
-                            if (col < end) st_global_16_policy(orow + col, o[0], pol);
-                            if (col + 8 < end) st_global_16_policy(orow + col + 8, o[1], pol);
+                            if (col < p.ncols) st_global_16_policy(orow + col, o[0], pol);
+                            if (col + 8 < p.ncols) st_global_16_policy(orow + col + 8, o[1], pol);
                         }
                     }
             }
@@ -303,12 +296,12 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
     if (warp == 1) tmem_dealloc_pair(tmem, 2 * kPN);
 }
 
-// Clusters resident at once (GG_OK), for the tile width's choice.
+// Clusters resident at once.
 template <bool B_MN>
 int pair_room(int* clusters) {
     static ClusterRoom rooms;
-    const int* room = nullptr;
-    const int rc = rooms.get(pair_kernel<B_MN>, kPThreads, kPairSmem, &room);
+    int room[kMaxCluster + 1];
+    const int rc = rooms.get(pair_kernel<B_MN>, kPairSmem, room);
     if (rc == GG_OK) *clusters = room[2];
     return rc;
 }
@@ -338,20 +331,7 @@ int lora_pair_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const uint
     int clusters = 0;
     const int rc = b_mn ? pair_room<true>(&clusters) : pair_room<false>(&clusters);
     if (rc != GG_OK) return rc;
-    // The tile width with the least rounds x columns a round, 16 columns' worth of
-    // every round being its own cost: the last round of 256-column tiles is often
-    // nearly empty.
-    p.width = kPN;
-    int64_t best = 0;
-    for (int w = kPN; w >= 192; w -= 32) {
-        const int64_t tiles = plan.units * ((ncols + w - 1) / w);
-        const int64_t cost = (tiles + clusters - 1) / clusters * (w + 16);
-        if (best == 0 || cost < best) {
-            best = cost;
-            p.width = w;
-        }
-    }
-    p.ntiles = static_cast<int>((ncols + p.width - 1) / p.width);
+    p.ntiles = static_cast<int>((ncols + kPN - 1) / kPN);
     p.tiles = plan.units * p.ntiles;
     p.out = out;
     p.st32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && ncols % 16 == 0;
@@ -364,8 +344,8 @@ int lora_pair_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const uint
         if (!encode_map_3d(&mE, ad, ncols, r, plan.L, ncols, ncols * r, 64, p.rpad)) return GG_ERR_CUDA;
         return launch_pair<true>(mX, mW, mU, mE, p, clusters, st);
     }
-    if (!encode_map_2d(&mW, W, Kred, ncols, Kred, kPK, p.width / 2)) return GG_ERR_CUDA;
-    if (!encode_map_3d(&mE, ad, r, ncols, plan.L, r, ncols * r, p.rpad, p.width / 2)) return GG_ERR_CUDA;
+    if (!encode_map_2d(&mW, W, Kred, ncols, Kred, kPK, kPN / 2)) return GG_ERR_CUDA;
+    if (!encode_map_3d(&mE, ad, r, ncols, plan.L, r, ncols * r, p.rpad, kPN / 2)) return GG_ERR_CUDA;
     return launch_pair<false>(mX, mW, mU, mE, p, clusters, st);
 }
 

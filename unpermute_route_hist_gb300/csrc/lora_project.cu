@@ -246,7 +246,7 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     float* part = reinterpret_cast<float*>(ring);
     const int q = warp & 3;
     const int row = q * 32 + lane;
-    // 8-column groups of a row are rotated by the row, against bank conflicts
+    // 4-column pieces of a row are rotated by the row, against bank conflicts
     if (warp >= 2 && q * 32 < rows) {
 #pragma unroll 1
         for (int c = 0; c < kRN; c += 32) {
@@ -255,11 +255,9 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             tmem_ld_wait();
             if (row < rows) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int piece = (((c / 8 + k / 2) ^ (row & 15)) << 1) | (k & 1);
-                    *reinterpret_cast<uint4*>(part + row * kRN + piece * 4) =
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<uint4*>(part + row * kRN + (((c / 4 + k) ^ (row & 31)) << 2)) =
                         make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                }
             }
             __syncwarp();
         }
@@ -268,14 +266,13 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     __syncthreads();
     cluster_sync();
     if (good) {
-        // the tile's 8-column pieces in turn: neighbouring threads store neighbouring pieces
-        for (int i = rank * kRThreads + threadIdx.x; i < rows * (kRN / 8); i += S * kRThreads) {
-            const int rr = i / (kRN / 8), g = i % (kRN / 8);
-            const int col = n0 + g * 8;
+        // a warp sums and stores one row's 128 columns at a time
+        for (int i = rank * kRThreads + threadIdx.x; i < rows * (kRN / 4); i += S * kRThreads) {
+            const int rr = i / (kRN / 4), g = i % (kRN / 4);
+            const int col = n0 + g * 4;
             if (col >= p.ncols) continue;
-            float s[8];
-            cluster_sum8(smem_u32(part + rr * kRN + ((g ^ (rr & 15)) << 3)), S, s);
-            *reinterpret_cast<uint4*>(p.out + (row0 + rr) * p.ncols + col) = pack_bf16x8(s);
+            const float4 s = cluster_sum4(smem_u32(part + rr * kRN + ((g ^ (rr & 31)) << 2)), S);
+            *reinterpret_cast<uint2*>(p.out + (row0 + rr) * p.ncols + col) = pack_bf16x4(s);
         }
     }
     __syncthreads();
@@ -290,8 +287,8 @@ template <bool B_MN>
 int launch_project(const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& u, const CUtensorMap& e,
                    const ProjectParams& p, cudaStream_t st) {
     static ClusterRoom rooms;
-    const int* room = nullptr;
-    const int rc = rooms.get(project_kernel<B_MN>, kRThreads, kProjectSmem, &room);
+    int room[kMaxCluster + 1];
+    const int rc = rooms.get(project_kernel<B_MN>, kProjectSmem, room);
     if (rc != GG_OK) return rc;
     // the widest split whose clusters are all resident at once
     const int64_t nb = (p.Kred + kRK - 1) / kRK;

@@ -63,6 +63,10 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     const int64_t item = blockIdx.x / S;
 
     pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmE);
+    }
     // rows without an adapter get zeros: this CTA's share of the units
     auto zero_bare_rows = [&]() {
         for (int64_t u = blockIdx.x; u < p.plan.units; u += gridDim.x) {
@@ -80,11 +84,12 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
             }
         }
     };
+    // (the grid has a cluster for every tile there could be: the entry exists)
+    const int4 tile = p.plan.tile[item / p.subs];
     if (item >= static_cast<int64_t>(*p.plan.ntile) * p.subs) {  // the whole cluster
         zero_bare_rows();
         return;
     }
-    const int4 tile = p.plan.tile[item / p.subs];
     const int a = tile.x, n = tile.z;
     const bool gather = tile.w < 0;
     const int c0 = static_cast<int>(item % p.subs) * p.take;
@@ -97,8 +102,6 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
         mbar_init(&ctl->done, 1);
         ctl->abort_flag = 0;
         fence_barrier_init();
-        tma_prefetch_desc(&tmX);
-        tma_prefetch_desc(&tmE);
     }
     if (warp == 1) {
         tmem_alloc(&ctl->tmem_base, kSN);
@@ -106,7 +109,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     }
     if (threadIdx.x >= 64) {
         const int i = threadIdx.x - 64;
-        if (i < n) ctl->row[i] = p.plan.order[tile.y + i];
+        if (i < n) ctl->row[i] = gather ? p.plan.order[tile.y + i] : tile.w + i;
     }
     tc_fence_before();
     __syncthreads();
@@ -231,21 +234,24 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     cluster_sync();
     if (good) {
         const float sc = p.scale ? p.scale[a] : 1.0f;
-        for (int i = rank * kSThreads + threadIdx.x; i < n * groups; i += S * kSThreads) {
-            const int rr = i / groups, c = (i % groups) * 8;
-            float s[8], rest[8];
-            cluster_sum8(smem_u32(part + rr * pitch + c), S, s);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                s[k] *= sc;
-                const float h = __bfloat162float(__float2bfloat16(s[k]));
-                rest[k] = fabsf(h) < __int_as_float(0x7f800000) ? s[k] - h : 0.f;
-            }
+        const int quads = groups * 2;
+        for (int i = rank * kSThreads + threadIdx.x; i < n * quads; i += S * kSThreads) {
+            const int rr = i / quads, c = (i % quads) * 4;
+            float4 s = cluster_sum4(smem_u32(part + rr * pitch + c), S);
+            s = make_float4(s.x * sc, s.y * sc, s.z * sc, s.w * sc);
             // U (V) is an operand of the tensor cores: bf16, and for the adapter
             // gradients, which sum it over tokens, its remainder as a second bf16
             const int64_t at = static_cast<int64_t>(ctl->row[rr]) * p.r + c0 + c;
-            *reinterpret_cast<uint4*>(p.out + at) = pack_bf16x8(s);
-            if (p.out_lo) *reinterpret_cast<uint4*>(p.out_lo + at) = pack_bf16x8(rest);
+            const uint2 hi = pack_bf16x4(s);
+            *reinterpret_cast<uint2*>(p.out + at) = hi;
+            if (p.out_lo) {
+                auto rest = [](float x) {
+                    const float h = __bfloat162float(__float2bfloat16(x));
+                    return fabsf(h) < __int_as_float(0x7f800000) ? x - h : 0.f;
+                };
+                *reinterpret_cast<uint2*>(p.out_lo + at) =
+                    pack_bf16x4(make_float4(rest(s.x), rest(s.y), rest(s.z), rest(s.w)));
+            }
         }
     }
     zero_bare_rows();
@@ -260,8 +266,8 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
 template <bool B_MN>
 int launch_shrink(const CUtensorMap& x, const CUtensorMap& e, const ShrinkParams& p, cudaStream_t st) {
     static ClusterRoom rooms;
-    const int* room = nullptr;
-    int rc = rooms.get(shrink_kernel<B_MN>, kSThreads, kShrinkSmem, &room);
+    int room[kMaxCluster + 1];
+    int rc = rooms.get(shrink_kernel<B_MN>, kShrinkSmem, room);
     if (rc != GG_OK) return rc;
     // The split: as many CTAs as are resident at once for the tiles a batch of
     // sequences has (whole tiles and half of the adapters' ragged ones).

@@ -19,6 +19,9 @@
 #include <cuda_fp16.h>
 
 namespace gg {
+
+int num_sms();
+
 namespace {
 
 constexpr int kRopeThreads = 256;
@@ -65,84 +68,113 @@ struct alignas(sizeof(E) * N) Vec {
     E e[N];
 };
 
-// dynamic shared memory: cos and sin of the CTA's tokens, [tokens][half] float2
+// Division of a 31-bit number by a number fixed at launch.
+struct FastDiv {
+    uint32_t d, mul, shift;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t x) : d(x), shift(0) {
+        while ((uint64_t(1) << shift) < x) ++shift;
+        mul = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - x)) / x + 1);
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
+// Dynamic shared memory: cos and sin of the CTA's tokens, [tokens][half] float2.  A
+// token's pairs are stored two by two across its pieces (pair k of piece v at
+// (k / 2) pieces + v), so that neighbouring threads read neighbouring 16 bytes:
+// in pair order every 16-byte read meets a 4-way bank conflict, which bound the
+// kernel.
 template <typename E, int PV, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
-    extern __shared__ float2 cs[];
+__global__ void __launch_bounds__(kRopeThreads)
+rope_kernel(const RopeParams p, const FastDiv per, const FastDiv heads, const FastDiv half) {
+    extern __shared__ __align__(16) float2 cs[];
+    using V = Vec<E, PV>;
+    constexpr int kPairs = PV > 1 ? 2 : 1;  // of a 16-byte read
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
     const int nt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.T - t0));
-    for (int i = threadIdx.x; i < nt * p.half; i += kRopeThreads) {
-        const int t = i / p.half, j = i - t * p.half;
+    const uint32_t turns = static_cast<uint32_t>(p.half / PV);  // rotated pieces of a head; then copied ones
+    for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(nt * p.half); i += kRopeThreads) {
+        const uint32_t t = half.div(i);
+        const int j = static_cast<int>(i - t * half.d);
         const int axis = (j >= p.bound[0]) + (j >= p.bound[1]) + (j >= p.bound[2]);
         const int64_t pos = p.pos[axis * p.T + t0 + t];
         // modulo one turn, as a signed fraction in [-1/2, 1/2)
         const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(pos) * static_cast<uint64_t>(p.step[j]));
         float s, c;
         sincospif(__ll2float_rn(turn) * 0x1p-63f, &s, &c);
-        cs[i] = make_float2(p.m * c, p.backward ? -p.m * s : p.m * s);
+        const uint32_t v = j / PV, k = j % PV;
+        cs[t * p.half + ((k / kPairs) * turns + v) * kPairs + k % kPairs] = make_float2(p.m * c, p.backward ? -p.m * s : p.m * s);
     }
     __syncthreads();
-    const uint32_t turns = static_cast<uint32_t>(p.half / PV);             // rotated pieces of a head
-    const uint32_t per = turns + static_cast<uint32_t>(p.tail / PV);       // and copied ones
-    const uint32_t heads = static_cast<uint32_t>(p.q.n + p.k.n);
-    const uint32_t items = static_cast<uint32_t>(nt) * heads * per;
+    const uint32_t items = static_cast<uint32_t>(nt) * heads.d * per.d;
     for (uint32_t i = threadIdx.x; i < items; i += kRopeThreads) {
-        const uint32_t th = i / per, v = i - th * per;
-        const uint32_t t = th / heads, h = th - t * heads;
+        const uint32_t th = per.div(i), v = i - th * per.d;
+        const uint32_t t = heads.div(th), h = th - t * heads.d;
         const bool isq = h < static_cast<uint32_t>(p.q.n);
         const RopeHeads& g = isq ? p.q : p.k;
         const int64_t hh = isq ? h : h - p.q.n;
         const E* x = static_cast<const E*>(g.x) + (t0 + t) * g.xt + hh * g.xh;
         E* o = static_cast<E*>(g.out) + (t0 + t) * g.ot + hh * g.oh;
-        if (v >= turns) {
-            const int at = 2 * p.half + static_cast<int>(v - turns) * PV;
-            *reinterpret_cast<Vec<E, PV>*>(o + at) = *reinterpret_cast<const Vec<E, PV>*>(x + at);
+        if (v >= turns) {  // copied: two pieces, half of the copied part apart
+            const uint32_t tail = static_cast<uint32_t>(p.tail / PV), copies = (tail + 1) / 2, c = v - turns;
+            const V* s = reinterpret_cast<const V*>(x + 2 * p.half);
+            V* d = reinterpret_cast<V*>(o + 2 * p.half);
+            const V z1 = s[c];
+            if (c + copies < tail) d[c + copies] = s[c + copies];
+            d[c] = z1;
             continue;
         }
-        const float2* a = cs + t * p.half + v * PV;
+        // the piece's two parts: pairs' first and second elements, or (interleaved) PV
+        // neighbouring elements and the PV after them
+        const uint32_t at = INTER ? 2 * v * PV : v * PV, off = INTER ? PV : p.half;
+        V z1 = *reinterpret_cast<const V*>(x + at), z2 = *reinterpret_cast<const V*>(x + at + off);
+        const float2* a = cs + t * p.half + v * kPairs;
+        E y[2 * PV];
         if (INTER) {
-            // 2 PV elements as two accesses of PV: aligned whenever PV elements are
-            Vec<E, PV>* d = reinterpret_cast<Vec<E, PV>*>(o + 2 * v * PV);
-            const Vec<E, PV>* z = reinterpret_cast<const Vec<E, PV>*>(x + 2 * v * PV);
-            E y[2 * PV];
-            Vec<E, PV> lo = z[0], hi = z[1];
 #pragma unroll
             for (int k = 0; k < PV; ++k) {
-                y[k] = lo.e[k];
-                y[PV + k] = hi.e[k];
+                y[k] = z1.e[k];
+                y[PV + k] = z2.e[k];
             }
-#pragma unroll
-            for (int k = 0; k < PV; ++k) {
-                const float x1 = to_f(y[2 * k]), x2 = to_f(y[2 * k + 1]);
-                y[2 * k] = from_f<E>(turn1(x1, x2, a[k]));
-                y[2 * k + 1] = from_f<E>(turn2(x1, x2, a[k]));
-            }
-#pragma unroll
-            for (int k = 0; k < PV; ++k) {
-                lo.e[k] = y[k];
-                hi.e[k] = y[PV + k];
-            }
-            d[0] = lo;
-            d[1] = hi;
-        } else {
-            Vec<E, PV> z1 = *reinterpret_cast<const Vec<E, PV>*>(x + v * PV);
-            Vec<E, PV> z2 = *reinterpret_cast<const Vec<E, PV>*>(x + p.half + v * PV);
-#pragma unroll
-            for (int k = 0; k < PV; ++k) {
-                const float x1 = to_f(z1.e[k]), x2 = to_f(z2.e[k]);
-                z1.e[k] = from_f<E>(turn1(x1, x2, a[k]));
-                z2.e[k] = from_f<E>(turn2(x1, x2, a[k]));
-            }
-            *reinterpret_cast<Vec<E, PV>*>(o + v * PV) = z1;
-            *reinterpret_cast<Vec<E, PV>*>(o + p.half + v * PV) = z2;
         }
+#pragma unroll
+        for (int k = 0; k < PV; k += kPairs) {
+            float2 c[kPairs];
+            if constexpr (kPairs == 2) {
+                const float4 c2 = *reinterpret_cast<const float4*>(a + k * turns);
+                c[0] = make_float2(c2.x, c2.y);
+                c[1] = make_float2(c2.z, c2.w);
+            } else {
+                c[0] = a[0];
+            }
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+                E& first = INTER ? y[2 * (k + e)] : z1.e[k + e];
+                E& second = INTER ? y[2 * (k + e) + 1] : z2.e[k + e];
+                const float x1 = to_f(first), x2 = to_f(second);
+                first = from_f<E>(turn1(x1, x2, c[e]));
+                second = from_f<E>(turn2(x1, x2, c[e]));
+            }
+        }
+        if (INTER) {
+#pragma unroll
+            for (int k = 0; k < PV; ++k) {
+                z1.e[k] = y[k];
+                z2.e[k] = y[PV + k];
+            }
+        }
+        *reinterpret_cast<V*>(o + at) = z1;
+        *reinterpret_cast<V*>(o + at + off) = z2;
     }
 }
 
 template <typename E, int PV>
 void launch_pv(const RopeParams& p, bool inter, unsigned grid, size_t smem, cudaStream_t st) {
-    if (inter) rope_kernel<E, PV, true><<<grid, kRopeThreads, smem, st>>>(p);
-    else rope_kernel<E, PV, false><<<grid, kRopeThreads, smem, st>>>(p);
+    const FastDiv per(static_cast<uint32_t>(p.half / PV + (p.tail / PV + 1) / 2));
+    const FastDiv heads(static_cast<uint32_t>(p.q.n + p.k.n));
+    const FastDiv half(static_cast<uint32_t>(p.half > 0 ? p.half : 1));
+    if (inter) rope_kernel<E, PV, true><<<grid, kRopeThreads, smem, st>>>(p, per, heads, half);
+    else rope_kernel<E, PV, false><<<grid, kRopeThreads, smem, st>>>(p, per, heads, half);
 }
 
 template <typename E>
@@ -164,13 +196,10 @@ int launch_rope(RopeParams p, bool inter, cudaStream_t st) {
     int pv = kMost;
     while (pv > 1 && !fits(pv)) pv /= 2;
     // tokens of a CTA: about two pieces a thread, while enough CTAs remain
-    const int64_t per = static_cast<int64_t>(p.q.n + p.k.n) * (p.half / pv + p.tail / pv);
+    const int64_t per = static_cast<int64_t>(p.q.n + p.k.n) * (p.half / pv + (p.tail / pv + 1) / 2);
     int64_t tok = (2 * kRopeThreads + per - 1) / per;
     if (tok > kRopeMaxTokens) tok = kRopeMaxTokens;
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    while (tok > 1 && (p.T + tok - 1) / tok < 2 * sms) --tok;
+    while (tok > 1 && (p.T + tok - 1) / tok < 2 * num_sms()) --tok;
     p.tokens = static_cast<int>(tok);
     const int64_t grid = (p.T + tok - 1) / tok;
     const size_t smem = static_cast<size_t>(tok) * p.half * sizeof(float2);

@@ -15,6 +15,7 @@ so the kernel reduces pos * f modulo one turn exactly.
 """
 from __future__ import annotations
 
+import ctypes
 import dataclasses
 import math
 
@@ -28,6 +29,12 @@ class RopeFreqs:
     rot_dim: int
     attention_scale: float          # factor on the turned elements
     sections: tuple | None = None   # pairs of each position axis, or None (one axis)
+
+    def __post_init__(self):
+        # what a call passes on, made once
+        axes = 1 if self.sections is None else len(self.sections)
+        object.__setattr__(self, "axes", axes)
+        object.__setattr__(self, "c_sections", (ctypes.c_int32 * axes)(*self.sections) if axes > 1 else None)
 
 
 def frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
