@@ -406,7 +406,7 @@ def lora_backward(dY, X, W, A, B, scale, plan: LoraPlan, U, *, want=(True, True,
     dX = _out(out, (T, K), torch.bfloat16, dev, "out") if want[0] else None
     dA = _out(out_da, (L, r, K), torch.bfloat16, dev, "out_da") if want[1] else None
     dB = _out(out_db, (L, N, r), torch.bfloat16, dev, "out_db") if want[2] else None
-    ws = _workspace(workspace, lora_backward_workspace_size(T, r) if want[0] or want[1] else 0, dev)
+    ws = _workspace(workspace, lora_backward_workspace_size(T, r), dev)
     rc = _lib.load().gg_lora_backward(dY.data_ptr(), X.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(), _p(scale),
                                       plan.buf.data_ptr(), U.data_ptr(), T, L, r, N, K, _p(dX), _p(dA), _p(dB),
                                       _p(ws), _nbytes(ws), _p(status), _stream(dev))

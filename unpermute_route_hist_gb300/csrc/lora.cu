@@ -19,6 +19,10 @@ int check_sizes(int64_t T, int L, int r, int64_t N, int64_t K) {
     return GG_OK;
 }
 
+// The backward's workspace: V, its remainder, the gradients' counters and partial sums.
+size_t v_bytes(int64_t T, int r) { return (static_cast<size_t>(T) * r * 2 + 255) / 256 * 256; }
+constexpr size_t kCounterBytes = (kGradCtas * sizeof(uint32_t) + 255) / 256 * 256;
+
 // Y (or dX) from its operands: 2-CTA tiles when they fill the GPU, else split tiles.
 int project(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, const uint16_t* ad,
             const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, int32_t* status, cudaStream_t st) {
@@ -63,14 +67,14 @@ int gg_lora_forward(const gg_bf16* X, const gg_bf16* W, const gg_bf16* A, const 
     if (!X || !A || (N > 0 && (!W || !B))) return GG_ERR_INVALID_ARG;
     if (!al16(X) || !al16(W) || !al16(A) || !al16(B)) return GG_ERR_UNSUPPORTED;
     const PlanView v = plan_view(const_cast<void*>(plan), T, L);
-    const int e = lora_shrink_launch(false, X, A, scale, v, K, r, U, nullptr, status, st);
+    const int e = lora_shrink_launch(false, X, A, scale, v, K, r, U, nullptr, nullptr, 0, status, st);
     if (e != GG_OK || N == 0) return e;
     return project(false, X, W, U, B, v, K, N, r, Y, status, st);
 }
 
 size_t gg_lora_backward_workspace_size(int64_t T, int r) {
     if (T < 0 || r < 1) return 0;
-    return 2 * ((static_cast<size_t>(T) * r * 2 + 255) / 256 * 256);
+    return 2 * v_bytes(T, r) + kCounterBytes + static_cast<size_t>(2 * kGradCtas) * 128 * r * sizeof(float);
 }
 
 int gg_lora_backward(const gg_bf16* dY, const gg_bf16* X, const gg_bf16* W, const gg_bf16* A, const gg_bf16* B,
@@ -93,16 +97,21 @@ int gg_lora_backward(const gg_bf16* dY, const gg_bf16* X, const gg_bf16* W, cons
     }
     if (!plan || !dY || !B || (dX && (!W || !A)) || (dA && !X) || (dB && !U)) return GG_ERR_INVALID_ARG;
     if (!al16(plan) || !al16(dY) || !al16(X) || !al16(W) || !al16(A) || !al16(B) || !al16(U)) return GG_ERR_UNSUPPORTED;
-    const bool need_v = dX || dA;
-    if (need_v && (!workspace || !al16(workspace) || workspace_bytes < gg_lora_backward_workspace_size(T, r)))
-        return GG_ERR_WORKSPACE;
+    if (!workspace || !al16(workspace) || workspace_bytes < gg_lora_backward_workspace_size(T, r)) return GG_ERR_WORKSPACE;
     const PlanView v = plan_view(const_cast<void*>(plan), T, L);
-    uint16_t* V = static_cast<uint16_t*>(workspace);
-    uint16_t* V_lo = need_v ? V + gg_lora_backward_workspace_size(T, r) / 4 : nullptr;
-    int e = GG_OK;
-    if (need_v) e = lora_shrink_launch(true, dY, B, scale, v, N, r, V, dA ? V_lo : nullptr, status, st);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    uint16_t* V = reinterpret_cast<uint16_t*>(ws);
+    uint16_t* V_lo = reinterpret_cast<uint16_t*>(ws + v_bytes(T, r));
+    uint32_t* counters = reinterpret_cast<uint32_t*>(ws + 2 * v_bytes(T, r));
+    float* sums = reinterpret_cast<float*>(ws + 2 * v_bytes(T, r) + kCounterBytes);
+    int e;
+    if (dX || dA)
+        e = lora_shrink_launch(true, dY, B, scale, v, N, r, V, dA ? V_lo : nullptr, counters, kGradCtas, status, st);
+    else
+        e = cuda_result(cudaMemsetAsync(counters, 0, kGradCtas * sizeof(uint32_t), st));
     if (e == GG_OK && dX) e = project(true, dY, W, V, A, v, N, K, r, dX, status, st);
-    if (e == GG_OK && (dA || dB)) e = lora_grad_launch(X, dY, U, V, V_lo, v, K, N, r, dA, dB, status, st);
+    if (e == GG_OK && (dA || dB))
+        e = lora_grad_launch(X, dY, U, V, V_lo, v, K, N, r, dA, dB, counters, sums, status, st);
     return e;
 }
 

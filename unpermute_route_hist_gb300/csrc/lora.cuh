@@ -31,6 +31,7 @@ constexpr int kLoraMaxRank = 256;
 //   start    [units][slots]     rows of that adapter in earlier units
 //   goff     [L + 1]            first position of each adapter's rows in order
 //   toff     [L + 1]            first tile of each adapter
+//   boff     [L + 1]            64-row blocks of the adapters before each
 //   order    [T]                rows sorted by adapter, ascending inside one
 //   tile     [max_tiles] int4   {adapter, position in order, rows, first row if the
 //                               rows are neighbours in memory, else -1}: up to 128
@@ -47,6 +48,7 @@ struct PlanView {
     int32_t* start;
     int32_t* goff;
     int32_t* toff;
+    int32_t* boff;
     int32_t* order;
     int4* tile;
 };
@@ -75,6 +77,7 @@ inline PlanView plan_view(void* buf, int64_t T, int L, size_t* bytes = nullptr) 
     v.start = static_cast<int32_t*>(take(v.units * v.slots, 4));
     v.goff = static_cast<int32_t*>(take(static_cast<int64_t>(L) + 1, 4));
     v.toff = static_cast<int32_t*>(take(static_cast<int64_t>(L) + 1, 4));
+    v.boff = static_cast<int32_t*>(take(static_cast<int64_t>(L) + 1, 4));
     v.order = static_cast<int32_t*>(take(T, 4));
     v.tile = static_cast<int4*>(take(v.max_tiles, 16));
     if (bytes) *bytes = at;
@@ -257,8 +260,10 @@ struct ClusterRoom {
 };
 
 // U = scale X A^T (B_MN false; A [L, r, K]) or V = scale dY B (B_MN true; B [L, N, r]).
+// zero (if any): zero_words 32-bit words that the launch also clears.
 int lora_shrink_launch(bool b_mn, const uint16_t* X, const uint16_t* ad, const float* scale, const PlanView& plan,
-                       int64_t Kred, int r, uint16_t* out, uint16_t* out_lo, int32_t* status, cudaStream_t st);
+                       int64_t Kred, int r, uint16_t* out, uint16_t* out_lo, uint32_t* zero, int zero_words,
+                       int32_t* status, cudaStream_t st);
 // Y = X W^T + U B^T (b_mn false) or dX = dY W + V A (b_mn true): split-reduction
 // clusters for few row tiles, 2-CTA pair tiles otherwise.
 int lora_project_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, const uint16_t* ad,
@@ -267,9 +272,12 @@ int lora_project_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const u
 int lora_pair_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, const uint16_t* ad,
                      const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, int32_t* status,
                      cudaStream_t st);
+// dA, dB (either may be null); counters: kGradCtas zeroed words, sums: the CTAs' partial
+// sums, 2 x kGradCtas x 128 x r floats.
+constexpr int kGradCtas = 320;
 int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, const uint16_t* V, const uint16_t* V_lo,
-                     const PlanView& plan, int64_t K, int64_t N, int r, uint16_t* dA, uint16_t* dB, int32_t* status,
-                     cudaStream_t st);
+                     const PlanView& plan, int64_t K, int64_t N, int r, uint16_t* dA, uint16_t* dB, uint32_t* counters,
+                     float* sums, int32_t* status, cudaStream_t st);
 int lora_plan_launch(const int32_t* ids, const PlanView& plan, int32_t* status, cudaStream_t st);
 
 }  // namespace gg

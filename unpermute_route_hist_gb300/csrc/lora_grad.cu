@@ -11,7 +11,14 @@
 // rows are neighbours in memory (a sequence's) is copied by TMA; any other (ids
 // in no order, the adapter's last rows) is gathered row by row with cp.async, rows
 // past the end as zeros, so nothing of another adapter's rows enters the sums.
-// Blocks are split over a cluster and the partial sums joined as in lora_shrink.cu.
+//
+// All blocks of all (adapter, chunk) items are one list, cut into equal shares, one
+// a CTA: adapters differ widely in tokens, and an item a CTA left the largest
+// adapter's items running alone (65 against 47 us for two draws of 8192 tokens).
+// The ring runs on from item to item; accumulators are double-buffered, so an item's
+// epilogue overlaps the next one's loads.  An item that ends in another CTA than it
+// began leaves fp32 partial sums, and whichever of its CTAs comes last adds them in
+// block order: nothing waits, and the bits do not depend on who that was.
 #include "lora.cuh"
 
 namespace gg {
@@ -19,14 +26,10 @@ namespace {
 
 constexpr int kGM = 128;            // columns of the wide source
 constexpr int kGK = 64;             // rows of a block
-constexpr int kGThreads = 192;      // producer, issuer, four gather / epilogue warps
+constexpr int kGThreads = 320;      // producer, issuer, four gather and four epilogue warps
 constexpr int kGWide = kGM * kGK * 2;
-constexpr int kGMaxStages = 6;
-// the partial sums fit the drained ring
-static_assert(73728 >= 4 * kGM * (32 + 4) && 73728 >= 4 * 32 * (kGM + 4), "ring");
-static_assert(98304 >= 4 * kGM * (64 + 4) && 98304 >= 4 * 64 * (kGM + 4), "ring");
-static_assert(196608 >= 4 * kGM * (kLoraMaxRank + 4) && 196608 >= 4 * kLoraMaxRank * (kGM + 4), "ring");
-
+constexpr int kGMaxStages = 8;
+constexpr int kGMinBlocks = 4;      // of a CTA's share
 
 struct GradSide {
     const uint16_t* wide;      // [T, cols]
@@ -43,15 +46,21 @@ struct GradParams {
     int r, chunk, nc;          // rank; width (16, 32, 64) and number of its pieces
     int stages;
     int stage_bytes;
+    uint32_t* counter;         // [CTA]: arrivals of the item that CTA began and did not end
+    float* sums;               // [CTA][2][r][128]
     int32_t* status;
 };
 
 struct GradCtl {
     uint64_t full[kGMaxStages];
     uint64_t empty[kGMaxStages];
-    uint64_t done;
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
+    int last;
+    int gathered[kGMaxStages];  // the stage's block was gathered by cp.async
 };
 
 struct GradMaps {
@@ -59,10 +68,30 @@ struct GradMaps {
     CUtensorMap narrow[3];     // V, V's remainder, U
 };
 
+// A CTA's share of the list, walked block by block: adapter a, chunk `tile` of both
+// sides' together, block b of the adapter's nb.
+struct GradWalk {
+    int a, tile, b, nb;
+    int32_t t0;  // the adapter's first row tile
+    int64_t at;  // position in the list
+};
+
+// Whether ok holds in all 128 threads of the epilogue (a barrier of theirs).
+__device__ __forceinline__ bool all_of_128(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(ok ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+
 // RING: bytes of the operand ring; CTAS: resident on an SM
 template <int RING, int CTAS>
 __global__ void __launch_bounds__(kGThreads, CTAS)
-grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int S) {
+grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -70,15 +99,9 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int
     GradCtl* ctl = &ctl_s;
     volatile int* abort_flag = &ctl->abort_flag;
     const int warp = warp_id(), lane = lane_id();
-    const int rank = static_cast<int>(cluster_ctarank());
-    const int64_t item = blockIdx.x / S;
     const int tiles = p.side[0].tiles + p.side[1].tiles;
-    const int a = static_cast<int>(item / tiles);
-    const int tile = static_cast<int>(item % tiles);
-    const int sd = tile < p.side[0].tiles ? 0 : 1;
-    const GradSide side = p.side[sd];
-    const int col0 = (sd == 0 ? tile : tile - p.side[0].tiles) * kGM;
     const int ncols = p.chunk * p.nc;  // accumulator columns
+    const int buf_cols = ncols <= 16 ? 16 : (ncols <= 32 ? 32 : (ncols <= 64 ? 64 : (ncols <= 128 ? 128 : 256)));
     const uint32_t piece_bytes = static_cast<uint32_t>(p.chunk) * kGK * 2;
 
     if (threadIdx.x == 0) {
@@ -86,70 +109,109 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int
             mbar_init(&ctl->full[s], 1 + 128);  // the producer, every gather thread
             mbar_init(&ctl->empty[s], 1);
         }
-        mbar_init(&ctl->done, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ctl->acc_full[b], 1);
+            mbar_init(&ctl->acc_empty[b], 4);
+        }
+        mbar_init(&ctl->drain, 1);
         ctl->abort_flag = 0;
         fence_barrier_init();
-        tma_prefetch_desc(&maps.wide[sd]);
+        for (int k = 0; k < 2; ++k)
+            if (p.side[k].tiles) tma_prefetch_desc(&maps.wide[k]);
     }
-    const int tcols = ncols <= 32 ? 32 : (ncols <= 64 ? 64 : (ncols <= 128 ? 128 : 256));
     if (warp == 1) {
-        tmem_alloc(&ctl->tmem_base, tcols);
+        tmem_alloc(&ctl->tmem_base, 2 * buf_cols);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const int count = p.plan.goff[a + 1] - p.plan.goff[a];
-    const int4* tiles_a = p.plan.tile + p.plan.toff[a];
-    const int nb = (count + kGK - 1) / kGK;
-    const int act = min(S, nb);  // ranks with blocks
-    const int lo = rank < act ? static_cast<int>(static_cast<int64_t>(nb) * rank / act) : 0;
-    const int hi = rank < act ? static_cast<int>(static_cast<int64_t>(nb) * (rank + 1) / act) : 0;
     const uint32_t tmem = ctl->tmem_base;
     const uint32_t ring0 = smem_u32(ring);
-    const int nnarrow = p.nc * side.parts;
-    // Block b is half b & 1 of tile b / 2.  Each role walks the tiles with the next
-    // one's entry already loaded.
-    static_assert(kTileRows == 2 * kGK, "two blocks a tile");
-    int4 cur = make_int4(0, 0, 0, 0), next = cur;
-    if (hi > lo) {
-        cur = tiles_a[lo / 2];
-        if (lo / 2 < (hi - 1) / 2) next = tiles_a[lo / 2 + 1];
-    }
-    auto advance = [&](int b) {  // to block b + 1
-        if ((b & 1) && b + 1 < hi) {
-            cur = next;
-            if ((b + 1) / 2 < (hi - 1) / 2) next = tiles_a[(b + 1) / 2 + 1];
+    const int nblocks = p.plan.boff[p.plan.L];
+    const int64_t total = static_cast<int64_t>(nblocks) * tiles;
+    // the CTAs that share the list: none without a block, else kGMinBlocks each
+    const int64_t fit = total / kGMinBlocks > 1 ? total / kGMinBlocks : 1;
+    const int64_t G = fit < gridDim.x ? fit : gridDim.x;
+    const bool idle = blockIdx.x >= G;
+    const int64_t lo = idle ? 0 : total * blockIdx.x / G, hi = idle ? 0 : total * (blockIdx.x + 1) / G;
+
+    // The list runs chunk by chunk through all adapters' blocks, so that blocks that have
+    // to be gathered (3x a copied one's time) fall to all CTAs alike.
+    auto start = [&]() {
+        GradWalk w{0, 0, 0, 0, 0, lo};
+        if (lo < hi) {
+            w.tile = static_cast<int>(lo / nblocks);
+            const int in = static_cast<int>(lo - static_cast<int64_t>(w.tile) * nblocks);
+            int x = 0, y = p.plan.L - 1;  // the last adapter whose blocks begin at or before it
+            while (x < y) {
+                const int mid = (x + y + 1) >> 1;
+                if (p.plan.boff[mid] <= in) x = mid; else y = mid - 1;
+            }
+            w.a = x;
+            w.b = in - p.plan.boff[x];
+            w.nb = p.plan.boff[x + 1] - p.plan.boff[x];
+            w.t0 = p.plan.toff[x];
         }
+        return w;
     };
-    auto by_tma = [&](int b) { return cur.w >= 0 && cur.z >= ((b & 1) + 1) * kGK; };
+    // to the next block; true if it begins another item
+    auto step = [&](GradWalk& w) {
+        if (++w.at >= hi) return true;
+        if (++w.b < w.nb) return false;
+        w.b = 0;
+        do {
+            if (++w.a == p.plan.L) {
+                w.a = 0;
+                ++w.tile;
+            }
+            w.nb = p.plan.boff[w.a + 1] - p.plan.boff[w.a];
+        } while (w.nb == 0);
+        w.t0 = p.plan.toff[w.a];
+        return true;
+    };
+    auto rows_of = [&](const GradWalk& w) { return p.plan.tile[w.t0 + w.b / 2]; };
+    // 64 whole rows, neighbours in memory (block b is half b & 1 of tile b / 2)
+    static_assert(kTileRows == 2 * kGK, "two blocks a tile");
+    auto by_tma = [&](const int4& t, int b) { return t.w >= 0 && t.z >= ((b & 1) + 1) * kGK; };
 
     if (warp == 0) {
         // --------------------------------------------------- TMA producer --
         if (lane == 0) {
-            int stage = 0, issued = 0;
+            int stage = 0;
             uint32_t phase = 0;
-            for (int b = lo; b < hi; ++b) {
+            int64_t issued = 0;
+            GradWalk w = start();
+            int4 t = w.at < hi ? rows_of(w) : make_int4(0, 0, 0, 0);
+            while (w.at < hi) {
+                const int sd = w.tile < p.side[0].tiles ? 0 : 1;
+                const int col0 = (sd == 0 ? w.tile : w.tile - p.side[0].tiles) * kGM;
+                const bool tma = by_tma(t, w.b);
+                const int32_t row = t.w + (w.b & 1) * kGK;
+                step(w);
+                if (w.at < hi) t = rows_of(w);  // the next block's, on its way while this one waits
                 if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) break;
                 uint64_t* bar = &ctl->full[stage];
-                if (by_tma(b)) {
+                ctl->gathered[stage] = !tma;
+                if (tma) {
+                    const int parts = sd == 0 ? p.side[0].parts : p.side[1].parts;
                     uint8_t* s = ring + stage * p.stage_bytes;
-                    const int32_t t = cur.w + (b & 1) * kGK;
-                    mbar_arrive_expect_tx(bar, kGWide + piece_bytes * nnarrow);
-                    tma_load_2d(s, &maps.wide[sd], bar, col0, t);
-                    tma_load_2d(s + kGWide / 2, &maps.wide[sd], bar, col0 + 64, t);
-                    for (int k = 0; k < nnarrow; ++k)
-                        tma_load_2d(s + kGWide + k * piece_bytes, &maps.narrow[sd == 0 ? k / p.nc : 2], bar,
-                                    (k % p.nc) * p.chunk, t);
+                    mbar_arrive_expect_tx(bar, kGWide + piece_bytes * (p.nc * parts));
+                    tma_load_2d(s, &maps.wide[sd], bar, col0, row);
+                    tma_load_2d(s + kGWide / 2, &maps.wide[sd], bar, col0 + 64, row);
+                    s += kGWide;
+                    for (int part = 0; part < parts; ++part)
+                        for (int k = 0; k < p.nc; ++k, s += piece_bytes)
+                            tma_load_2d(s, &maps.narrow[sd == 0 ? part : 2], bar, k * p.chunk, row);
                 } else {
                     mbar_arrive(bar);
                 }
-                advance(b);
                 ++issued;
                 if (++stage == p.stages) { stage = 0; phase ^= 1u; }
             }
-            // every copy has landed before the ring is reused or the CTA exits
-            for (int j = 0; j < min(issued, p.stages); ++j) {
+            // every copy has landed before the CTA exits
+            const int64_t pend = issued < p.stages ? issued : p.stages;
+            for (int64_t j = 0; j < pend; ++j) {
                 if (--stage < 0) { stage = p.stages - 1; phase ^= 1u; }
                 int dummy = 0;
                 mbar_wait(&ctl->full[stage], phase, reinterpret_cast<volatile int*>(&dummy), p.status);
@@ -158,169 +220,275 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p, const int
         __syncwarp();
     } else if (warp == 1) {
         // ----------------------------------------------------- MMA issuer --
-        if (lane == 0 && hi > lo) {
+        if (lane == 0) {
             const uint32_t idesc = idesc_bf16_f32_n(kGM, ncols, 1, 1);
+            // descriptors of stage 0; an address advances by its bytes / 16
+            const uint64_t wide0 = smem_desc(ring0, kGWide / 2, 1024, kLayoutSw128);
+            const uint64_t narrow0 = mnmajor_desc(ring0 + kGWide, 2 * p.chunk, piece_bytes);
+            const uint32_t narrow_step = 2 * p.chunk, part_step = p.nc * piece_bytes / 16;
             int stage = 0;
-            uint32_t phase = 0;
-            bool any_mma = false;
-            for (int b = lo; b < hi; ++b) {
+            uint32_t phase = 0, item = 0;
+            bool any_mma = false, first = true;
+            for (GradWalk w = start(); w.at < hi;) {
+                const uint32_t buf = item & 1u;
+                const int parts = w.tile < p.side[0].tiles ? p.side[0].parts : p.side[1].parts;
+                if (first && !mbar_wait(&ctl->acc_empty[buf], ((item >> 1) & 1u) ^ 1u, abort_flag, p.status)) break;
                 if (!mbar_wait(&ctl->full[stage], phase, abort_flag, p.status)) break;
                 tc_fence_after();
-                fence_proxy_async_smem();  // gathered rows are generic-proxy writes
-                const uint32_t s = ring0 + stage * p.stage_bytes;
-                for (int part = 0; part < side.parts; ++part) {
-                    const uint32_t sN = s + kGWide + part * p.nc * piece_bytes;
+                // gathered rows are generic-proxy writes
+                if (*reinterpret_cast<volatile int*>(&ctl->gathered[stage])) fence_proxy_async_smem();
+                const uint32_t at = stage * p.stage_bytes / 16;
+                const uint32_t d = tmem + buf * buf_cols;
+#pragma unroll
+                for (int ks = 0; ks < kGK / 16; ++ks)
+                    umma_bf16(d, wide0 + at + ks * 128, narrow0 + at + ks * narrow_step, idesc,
+                              (!first || ks > 0) ? 1u : 0u);
+                if (parts == 2) {
 #pragma unroll
                     for (int ks = 0; ks < kGK / 16; ++ks)
-                        umma_bf16(tmem, smem_desc(s + ks * 2048, kGWide / 2, 1024, kLayoutSw128),
-                                  mnmajor_desc(sN + ks * 32 * p.chunk, 2 * p.chunk, piece_bytes), idesc,
-                                  (b > lo || part > 0 || ks > 0) ? 1u : 0u);
+                        umma_bf16(d, wide0 + at + ks * 128, narrow0 + at + part_step + ks * narrow_step, idesc, 1u);
                 }
                 umma_commit(&ctl->empty[stage]);
                 any_mma = true;
                 if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+                first = step(w);
+                if (first) {
+                    umma_commit(&ctl->acc_full[buf]);
+                    ++item;
+                }
             }
-            if (any_mma) umma_commit(&ctl->done);
-            else mbar_arrive(&ctl->done);
+            if (any_mma) {
+                umma_commit(&ctl->drain);
+                int dummy = 0;
+                mbar_wait(&ctl->drain, 0, reinterpret_cast<volatile int*>(&dummy), p.status);
+            }
         }
         __syncwarp();
-    } else {
+    } else if (warp < 6) {
         // ---------------------------------------------------- row gathers --
         const int gt = threadIdx.x - 64;  // 0 .. 127
         int stage = 0;
         uint32_t phase = 0;
-        for (int b = lo; b < hi; ++b) {
+        // 16 pieces of 8 columns a row of the wide source, 8 rows a step; chunk / 8 of the
+        // narrow one's, 128 / (chunk / 8) rows a step
+        const int pc = gt & 15;
+        const int npc = p.chunk / 8, np = gt % npc, nstep = 128 / npc;
+        // a block's rows of this thread, loaded one block ahead
+        struct Rows {
+            int32_t wide[kGK / 8], narrow[kGK / 16];
+        };
+        auto load_rows = [&](const int4& t, int b, Rows& r) {
+            const int off = (b & 1) * kGK, valid = t.z - off;
+            auto token = [&](int rr) {  // of the block's row rr
+                return rr >= valid ? -1 : (t.w >= 0 ? t.w + off + rr : p.plan.order[t.y + off + rr]);
+            };
+#pragma unroll
+            for (int j = 0; j < kGK / 8; ++j) r.wide[j] = token((gt >> 4) + 8 * j);
+#pragma unroll
+            for (int j = 0; j < kGK / 16; ++j) {
+                const int rr = gt / npc + nstep * j;
+                r.narrow[j] = rr < kGK ? token(rr) : -1;
+            }
+        };
+        GradWalk w = start();
+        Rows rows;
+        bool tma = true;
+        if (w.at < hi) {
+            const int4 t = rows_of(w);
+            tma = by_tma(t, w.b);
+            if (!tma) load_rows(t, w.b, rows);
+        }
+        while (w.at < hi) {
+            const bool now_tma = tma;
+            const Rows now = rows;
+            const int sd = w.tile < p.side[0].tiles ? 0 : 1;
+            const int col0 = (sd == 0 ? w.tile : w.tile - p.side[0].tiles) * kGM;
+            step(w);
+            if (w.at < hi) {
+                const int4 t = rows_of(w);
+                tma = by_tma(t, w.b);
+                if (!tma) load_rows(t, w.b, rows);
+            }
             if (!warp_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status, 32)) break;
-            if (by_tma(b)) {
+            if (now_tma) {
                 mbar_arrive(&ctl->full[stage]);
             } else {
+                const GradSide& side = p.side[sd];
                 const uint32_t s = ring0 + stage * p.stage_bytes;
-                const int off = (b & 1) * kGK, valid = cur.z - off;
-                auto token = [&](int rr) {  // of the block's row rr
-                    return rr >= valid ? -1 : (cur.w >= 0 ? cur.w + off + rr : p.plan.order[cur.y + off + rr]);
-                };
-                // 16 pieces of 8 columns a row of the wide source, 8 rows a step
-                const int pc = gt & 15;
                 const bool in = col0 + pc * 8 < side.cols;
-                int32_t tok[kGK / 8];
-#pragma unroll
-                for (int j = 0; j < kGK / 8; ++j) tok[j] = token((gt >> 4) + 8 * j);
 #pragma unroll
                 for (int j = 0; j < kGK / 8; ++j) {
                     const int rr = (gt >> 4) + 8 * j;
-                    const bool v = in && tok[j] >= 0;
+                    const bool v = in && now.wide[j] >= 0;
                     cp_async_16(s + (pc >> 3) * (kGWide / 2) + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4),
-                                v ? side.wide + static_cast<int64_t>(tok[j]) * side.cols + col0 + pc * 8 : side.wide,
+                                v ? side.wide + static_cast<int64_t>(now.wide[j]) * side.cols + col0 + pc * 8 : side.wide,
                                 v ? 16u : 0u);
                 }
-                // narrow: chunk / 8 pieces a row, swizzled over the row's width as TMA does
-                // (16-byte piece index XOR address bits 7 and up)
-                const int npc = p.chunk / 8;
-                const int np = gt % npc, rows_a_step = 128 / npc;
-                for (int rr = gt / npc; rr < kGK; rr += rows_a_step) {
-                    const int32_t t = token(rr);
+                // swizzled over the row's width as TMA does (16-byte piece index XOR address
+                // bits 7 and up)
+#pragma unroll
+                for (int j = 0; j < kGK / 16; ++j) {
+                    const int rr = gt / npc + nstep * j;
+                    if (rr >= kGK) break;
                     const uint32_t flip = static_cast<uint32_t>((rr * p.chunk * 2) >> 7) & (npc - 1);
-                    for (int k = 0; k < nnarrow; ++k) {
-                        const int c = (k % p.nc) * p.chunk + np * 8;
-                        const uint16_t* src = side.narrow[k / p.nc];
-                        const bool v = t >= 0 && c < p.r;
-                        cp_async_16(s + kGWide + k * piece_bytes + rr * p.chunk * 2 + ((np ^ flip) << 4),
-                                    v ? src + static_cast<int64_t>(t) * p.r + c : src, v ? 16u : 0u);
-                    }
+                    uint32_t to = s + kGWide + rr * p.chunk * 2 + ((np ^ flip) << 4);
+                    for (int part = 0; part < side.parts; ++part)
+                        for (int k = 0; k < p.nc; ++k, to += piece_bytes) {
+                            const int c = k * p.chunk + np * 8;
+                            const uint16_t* src = side.narrow[part];
+                            const bool v = now.narrow[j] >= 0 && c < p.r;
+                            cp_async_16(to, v ? src + static_cast<int64_t>(now.narrow[j]) * p.r + c : src, v ? 16u : 0u);
+                        }
                 }
                 cp_async_mbar_arrive(&ctl->full[stage]);
             }
-            advance(b);
             if (++stage == p.stages) { stage = 0; phase ^= 1u; }
         }
         cp_async_wait<0>();
+    } else {
+        // ------------------------------------------------------- epilogue --
+        const int q = warp & 3, row = q * 32 + lane;  // this thread's wide column
+        uint32_t item = 0;
+        for (GradWalk w = start(); w.at < hi; ++item) {
+            const uint32_t buf = item & 1u;
+            // the item, and the CTAs that hold its blocks
+            const int a = w.a, tile = w.tile;
+            const int64_t i_lo = w.at - w.b, i_hi = i_lo + w.nb;
+            const int64_t c_lo = ((i_lo + 1) * G - 1) / total, c_hi = (i_hi * G - 1) / total;
+            w.at = i_hi - 1 < hi ? i_hi - 1 : hi - 1;
+            w.b = w.nb - 1;
+            step(w);
+            const int sd = tile < p.side[0].tiles ? 0 : 1;
+            const GradSide& side = p.side[sd];
+            const int col = (sd == 0 ? tile : tile - p.side[0].tiles) * kGM + row;
+            // eight rank columns of this wide column to the gradient
+            auto store = [&](int c, const float (&v)[8]) {
+                if (col >= side.cols) return;
+                if (sd == 0) {
+                    uint16_t* o = side.out + (static_cast<int64_t>(a) * p.r + c) * side.cols + col;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        reinterpret_cast<__nv_bfloat16*>(o)[static_cast<int64_t>(k) * side.cols] = __float2bfloat16(v[k]);
+                } else {
+                    *reinterpret_cast<uint4*>(side.out + (static_cast<int64_t>(a) * side.cols + col) * p.r + c) =
+                        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                   pack_bf16x2(v[6], v[7]));
+                }
+            };
+            const size_t slot = static_cast<size_t>(kGM) * p.r;
+            // slot 1 of the CTA an item begins in, slot 0 of those it goes on in
+            float* mine = c_lo == c_hi ? nullptr : p.sums + (2 * blockIdx.x + (blockIdx.x == c_lo ? 1 : 0)) * slot + row;
+            // the four warps go on, or give up, together
+            const bool ok = warp_wait(&ctl->acc_full[buf], (item >> 1) & 1u, abort_flag, p.status, 64);
+            if (!all_of_128(ok)) break;
+            tc_fence_after();
+            for (int c = 0; c < p.r; c += 8) {
+                uint32_t u[8];
+                tmem_ld_32x32b_x8(tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * buf_cols + c, u);
+                tmem_ld_wait();
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(u[k]);
+                if (mine) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) __stcg(mine + (c + k) * kGM, v[k]);
+                } else {
+                    store(c, v);
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->acc_empty[buf]);
+            if (mine) {
+                // the four warps' sums are out before the arrival is counted
+                __threadfence();
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (warp == 6 && lane == 0) {
+                    uint32_t before;
+                    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(p.counter + c_lo) : "memory");
+                    ctl->last = before == static_cast<uint32_t>(c_hi - c_lo) ? 1 : 0;
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                const bool last = *reinterpret_cast<volatile int*>(&ctl->last) != 0;
+                if (last) {
+                    __threadfence();
+                    for (int c = 0; c < p.r; c += 8) {
+                        float v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = 0.f;
+                        for (int64_t j = c_lo; j <= c_hi; ++j) {
+                            const float* part = p.sums + (2 * j + (j == c_lo ? 1 : 0)) * slot + row;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) v[k] += __ldcg(part + (c + k) * kGM);
+                        }
+                        store(c, v);
+                    }
+                }
+                // (ctl->last is rewritten only after the next item's first barrier, which
+                // every reader reaches after reading it)
+            }
+        }
     }
 
-    // -------------------------------------------- partial sums to the cluster --
-    bool good = true;
-    if (hi > lo) good = warp_wait(&ctl->done, 0, abort_flag, p.status);
-    tc_fence_after();
-    __syncthreads();
-    float* part = reinterpret_cast<float*>(ring);
-    // dA is stored along the wide columns (pitch kGM), dB along the rank
-    const int pitch = sd == 0 ? kGM + 4 : p.r + 4;
-    if (warp >= 2 && hi > lo) {
-        const int q = warp & 3, row = q * 32 + lane;
-        for (int c = 0; c < p.r; c += 8) {
-            uint32_t v[8];
-            tmem_ld_32x32b_x8(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, v);
-            tmem_ld_wait();
-            if (sd == 0) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) part[(c + k) * pitch + row] = __uint_as_float(v[k]);
-            } else {
-                *reinterpret_cast<uint4*>(part + row * pitch + c) = make_uint4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<uint4*>(part + row * pitch + c + 4) = make_uint4(v[4], v[5], v[6], v[7]);
-            }
+    // adapters without tokens get zeros
+    for (int a = blockIdx.x; a < p.plan.L; a += gridDim.x) {
+        if (p.plan.boff[a + 1] != p.plan.boff[a]) continue;
+        for (int k = 0; k < 2; ++k) {
+            if (!p.side[k].tiles) continue;
+            const int64_t n = static_cast<int64_t>(p.r) * p.side[k].cols;
+            for (int64_t i = threadIdx.x * 8; i < n; i += kGThreads * 8)
+                *reinterpret_cast<uint4*>(p.side[k].out + a * n + i) = make_uint4(0, 0, 0, 0);
         }
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();
-    if (good) {
-        const int wide = min(kGM, side.cols - col0);
-        if (sd == 0) {
-            const int quads = wide / 4;
-            for (int i = rank * kGThreads + threadIdx.x; i < p.r * quads; i += S * kGThreads) {
-                const int c = i / quads, k = (i % quads) * 4;
-                *reinterpret_cast<uint2*>(side.out + (static_cast<int64_t>(a) * p.r + c) * side.cols + col0 + k) =
-                    pack_bf16x4(cluster_sum4(smem_u32(part + c * pitch + k), act));
-            }
-        } else {
-            const int quads = p.r / 4;
-            for (int i = rank * kGThreads + threadIdx.x; i < wide * quads; i += S * kGThreads) {
-                const int n = i / quads, c = (i % quads) * 4;
-                *reinterpret_cast<uint2*>(side.out + (static_cast<int64_t>(a) * side.cols + col0 + n) * p.r + c) =
-                    pack_bf16x4(cluster_sum4(smem_u32(part + n * pitch + c), act));
-            }
-        }
-    }
-    __syncthreads();
-    cluster_sync();  // no CTA leaves while another may still read its sums
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, tcols);
+        tmem_dealloc(tmem, 2 * buf_cols);
     }
 }
 
 template <int RING, int CTAS>
 int launch_grad(const GradMaps& m, GradParams p, cudaStream_t st) {
     constexpr size_t smem = 1024 + RING;
-    static ClusterRoom rooms;
-    int room[kMaxCluster + 1];
-    const int rc = rooms.get(grad_kernel<RING, CTAS>, smem, room);
-    if (rc != GG_OK) return rc;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) { record_cuda_error(e); return GG_ERR_CUDA; }
+    if (dev < 0 || dev >= 64) dev = 0;
+    static std::atomic<bool> smem_set[64];
+    if (!smem_set[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(grad_kernel<RING, CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(smem));
+        if (e != cudaSuccess) { record_cuda_error(e); return GG_ERR_CUDA; }
+        smem_set[dev].store(true, std::memory_order_release);
+    }
     p.stages = RING / p.stage_bytes;
     if (p.stages > kGMaxStages) p.stages = kGMaxStages;
-    // The split: until the CTAs fill the GPU twice, at least two blocks of a mean
-    // adapter each.
-    const int64_t items = static_cast<int64_t>(p.plan.L) * (p.side[0].tiles + p.side[1].tiles);
-    const int64_t blocks = p.plan.T / kGK / p.plan.L;
-    int S = kMaxCluster;
-    while (S > 1 && (items > 2 * room[S] || S * 2 > blocks)) S /= 2;
-    if (items * S >= (int64_t(1) << 31)) return GG_ERR_UNSUPPORTED;
-    ClusterLaunch l(items * S, kGThreads, smem, S, false, st);
+    // every CTA resident at once, none with less than kGMinBlocks blocks of the
+    // blocks there can be
+    const int64_t most = p.plan.T / kGK + (p.plan.T < p.plan.L ? p.plan.T : p.plan.L);
+    int64_t G = most * (p.side[0].tiles + p.side[1].tiles) / kGMinBlocks;
+    if (G > int64_t(CTAS) * num_sms()) G = int64_t(CTAS) * num_sms();
+    if (G > kGradCtas) G = kGradCtas;
+    if (G < 1) G = 1;
     clear_pending_launch_error();
-    const cudaError_t err = cudaLaunchKernelEx(&l.cfg, grad_kernel<RING, CTAS>, m, p, S);
-    if (err != cudaSuccess) { record_cuda_error(err); return GG_ERR_CUDA; }
+    grad_kernel<RING, CTAS><<<static_cast<unsigned>(G), kGThreads, smem, st>>>(m, p);
     return launch_result();
 }
 
 }  // namespace
 
 int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, const uint16_t* V, const uint16_t* V_lo,
-                     const PlanView& plan, int64_t K, int64_t N, int r, uint16_t* dA, uint16_t* dB, int32_t* status,
-                     cudaStream_t st) {
+                     const PlanView& plan, int64_t K, int64_t N, int r, uint16_t* dA, uint16_t* dB, uint32_t* counters,
+                     float* sums, int32_t* status, cudaStream_t st) {
     GradParams p{};
     p.plan = plan;
     p.r = r;
     p.chunk = rank_pad(r);
     p.nc = (r + p.chunk - 1) / p.chunk;
+    p.counter = counters;
+    p.sums = sums;
     p.status = status;
     if (dA)
         p.side[0] = GradSide{X, {V, V_lo}, 2, static_cast<int>(K), static_cast<int>((K + kGM - 1) / kGM), dA};
@@ -337,9 +505,7 @@ int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, c
         if (!encode_map_2d(&m.wide[1], dY, N, plan.T, N, 64, kGK)) return GG_ERR_CUDA;
         if (!encode_map_2d(&m.narrow[2], U, r, plan.T, r, p.chunk, kGK)) return GG_ERR_CUDA;
     }
-    // rings of at least three stages while two CTAs fit an SM (ranks up to 64), three
-    // CTAs for ranks up to 32
-    if (p.chunk <= 32) return launch_grad<73728, 3>(m, p, st);
+    // two CTAs an SM for ranks up to 64, one above
     return p.nc == 1 ? launch_grad<98304, 2>(m, p, st) : launch_grad<196608, 1>(m, p, st);
 }
 

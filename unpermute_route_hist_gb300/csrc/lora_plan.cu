@@ -89,31 +89,36 @@ __global__ void __launch_bounds__(128) plan_groups_kernel(PlanView v) {
     if (lane == 0) v.goff[a + 1] = run;
 }
 
-// One warp: exclusive prefixes of the adapters' row counts (in place) and tiles.
+// One warp: exclusive prefixes of the adapters' rows (in place), tiles and blocks.
 __global__ void __launch_bounds__(32) plan_scan_kernel(PlanView v) {
     const int lane = lane_id();
-    int rows = 0, tiles = 0;
+    int rows = 0, tiles = 0, blocks = 0;
     for (int a0 = 0; a0 < v.L; a0 += 32) {
         const int a = a0 + lane;
         const int c = a < v.L ? v.goff[a + 1] : 0;
-        int x = c, y = (c + kTileRows - 1) / kTileRows;
+        int x = c, y = (c + kTileRows - 1) / kTileRows, z = (c + 63) / 64;
         for (int d = 1; d < 32; d <<= 1) {
             const int xs = __shfl_up_sync(0xffffffffu, x, d), ys = __shfl_up_sync(0xffffffffu, y, d);
+            const int zs = __shfl_up_sync(0xffffffffu, z, d);
             if (lane >= d) {
                 x += xs;
                 y += ys;
+                z += zs;
             }
         }
         if (a < v.L) {
             v.goff[a + 1] = rows + x;
             v.toff[a + 1] = tiles + y;
+            v.boff[a + 1] = blocks + z;
         }
         rows += __shfl_sync(0xffffffffu, x, 31);
         tiles += __shfl_sync(0xffffffffu, y, 31);
+        blocks += __shfl_sync(0xffffffffu, z, 31);
     }
     if (lane == 0) {
         v.goff[0] = 0;
         v.toff[0] = 0;
+        v.boff[0] = 0;
         *v.ntile = tiles;
     }
 }

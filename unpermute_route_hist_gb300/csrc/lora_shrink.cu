@@ -33,6 +33,8 @@ struct ShrinkParams {
     const float* scale;
     uint16_t* out;
     uint16_t* out_lo;  // the rounding's remainder, in bf16 (or null)
+    uint32_t* zero;    // words to clear for the kernels after
+    int zero_words;
     int32_t* status;
 };
 
@@ -69,6 +71,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
     }
     // rows without an adapter get zeros: this CTA's share of the units
     auto zero_bare_rows = [&]() {
+        for (int i = blockIdx.x * kSThreads + threadIdx.x; i < p.zero_words; i += gridDim.x * kSThreads) p.zero[i] = 0;
         for (int64_t u = blockIdx.x; u < p.plan.units; u += gridDim.x) {
             for (int w = warp; w < kUnitWords; w += kSThreads / 32) {
                 const int64_t t0 = u * kUnit + w * 32;
@@ -288,7 +291,8 @@ int launch_shrink(const CUtensorMap& x, const CUtensorMap& e, const ShrinkParams
 }  // namespace
 
 int lora_shrink_launch(bool b_mn, const uint16_t* X, const uint16_t* ad, const float* scale, const PlanView& plan,
-                       int64_t Kred, int r, uint16_t* out, uint16_t* out_lo, int32_t* status, cudaStream_t st) {
+                       int64_t Kred, int r, uint16_t* out, uint16_t* out_lo, uint32_t* zero, int zero_words,
+                       int32_t* status, cudaStream_t st) {
     ShrinkParams p{};
     p.plan = plan;
     p.X = X;
@@ -300,6 +304,8 @@ int lora_shrink_launch(bool b_mn, const uint16_t* X, const uint16_t* ad, const f
     p.scale = scale;
     p.out = out;
     p.out_lo = out_lo;
+    p.zero = zero;
+    p.zero_words = zero ? zero_words : 0;
     p.status = status;
     const int rows = plan.T >= kSM ? kSM : static_cast<int>((plan.T + 7) / 8 * 8);
     p.a_slot = rows * 128;
