@@ -32,6 +32,9 @@ constexpr int kLoraMaxRank = 256;
 //   goff     [L + 1]            first position of each adapter's rows in order
 //   toff     [L + 1]            first tile of each adapter
 //   boff     [L + 1]            64-row blocks of the adapters before each
+//   block    [max_blocks] int4  {adapter, position in order, rows, first row if the
+//                               rows are neighbours, else -1}: up to 64 rows of one
+//                               adapter; of an adapter's last, rows + kLastBlock
 //   order    [T]                rows sorted by adapter, ascending inside one
 //   tile     [max_tiles] int4   {adapter, position in order, rows, first row if the
 //                               rows are neighbours in memory, else -1}: up to 128
@@ -39,7 +42,7 @@ constexpr int kLoraMaxRank = 256;
 struct PlanView {
     int64_t T;
     int L, slots;
-    int64_t units, max_tiles;
+    int64_t units, max_tiles, max_blocks;
     int32_t* ntile;
     int32_t* cnt;
     int32_t* gid;
@@ -51,9 +54,12 @@ struct PlanView {
     int32_t* boff;
     int32_t* order;
     int4* tile;
+    int4* block;
 };
 
 constexpr int kTileRows = 128;
+constexpr int kBlockRows = 64;
+constexpr int kLastBlock = 1 << 16;
 
 // The plan's layout over buf (null: only the size matters); its bytes in *bytes.
 inline PlanView plan_view(void* buf, int64_t T, int L, size_t* bytes = nullptr) {
@@ -63,6 +69,7 @@ inline PlanView plan_view(void* buf, int64_t T, int L, size_t* bytes = nullptr) 
     v.units = (T + kUnit - 1) / kUnit;
     v.slots = L < kUnit ? L : kUnit;
     v.max_tiles = T / kTileRows + (T < L ? T : L);
+    v.max_blocks = T / kBlockRows + (T < L ? T : L);
     size_t at = 0;
     auto take = [&](int64_t n, int64_t size) {
         void* p = static_cast<uint8_t*>(buf) + at;
@@ -80,6 +87,7 @@ inline PlanView plan_view(void* buf, int64_t T, int L, size_t* bytes = nullptr) 
     v.boff = static_cast<int32_t*>(take(static_cast<int64_t>(L) + 1, 4));
     v.order = static_cast<int32_t*>(take(T, 4));
     v.tile = static_cast<int4*>(take(v.max_tiles, 16));
+    v.block = static_cast<int4*>(take(v.max_blocks, 16));
     if (bytes) *bytes = at;
     return v;
 }

@@ -7,7 +7,7 @@
 // Bound by reading X and dY once; the MMAs run with the wide columns as M and the
 // rank as N.
 //
-// The rows are the plan's tiles, in blocks of 64 rows of one adapter.  A block whose
+// The rows are the plan's blocks of up to 64 rows of one adapter.  A block whose
 // rows are neighbours in memory (a sequence's) is copied by TMA; any other (ids
 // in no order, the adapter's last rows) is gathered row by row with cp.async, rows
 // past the end as zeros, so nothing of another adapter's rows enters the sums.
@@ -25,7 +25,7 @@ namespace gg {
 namespace {
 
 constexpr int kGM = 128;            // columns of the wide source
-constexpr int kGK = 64;             // rows of a block
+constexpr int kGK = kBlockRows;     // rows of a block
 constexpr int kGThreads = 320;      // producer, issuer, four gather and four epilogue warps
 constexpr int kGWide = kGM * kGK * 2;
 constexpr int kGMaxStages = 8;
@@ -43,7 +43,7 @@ struct GradSide {
 struct GradParams {
     PlanView plan;
     GradSide side[2];          // dA, dB
-    int r, chunk, nc;          // rank; width (16, 32, 64) and number of its pieces
+    int r, nc;                 // rank; number of its pieces
     int stages;
     int stage_bytes;
     uint32_t* counter;         // [CTA]: arrivals of the item that CTA began and did not end
@@ -60,19 +60,22 @@ struct GradCtl {
     uint32_t tmem_base;
     int abort_flag;
     int last;
-    int gathered[kGMaxStages];  // the stage's block was gathered by cp.async
+    int kind[kGMaxStages];  // of the stage's block: kGathered | kItemEnd | kTwoParts
 };
+
+constexpr int kGathered = 1;  // by cp.async
+constexpr int kItemEnd = 2;   // the last of its item here
+constexpr int kTwoParts = 4;  // the narrow operand has a remainder
 
 struct GradMaps {
     CUtensorMap wide[2];
     CUtensorMap narrow[3];     // V, V's remainder, U
 };
 
-// A CTA's share of the list, walked block by block: adapter a, chunk `tile` of both
+// A CTA's share of the list, walked item by item: adapter a, chunk `tile` of both
 // sides' together, block b of the adapter's nb.
 struct GradWalk {
     int a, tile, b, nb;
-    int32_t t0;  // the adapter's first row tile
     int64_t at;  // position in the list
 };
 
@@ -88,8 +91,9 @@ __device__ __forceinline__ bool all_of_128(bool ok) {
     return r != 0;
 }
 
-// RING: bytes of the operand ring; CTAS: resident on an SM
-template <int RING, int CTAS>
+// RING: bytes of the operand ring; CTAS: resident on an SM; CHUNK: rank columns of a
+// narrow piece (16, 32 or 64)
+template <int RING, int CTAS, int CHUNK>
 __global__ void __launch_bounds__(kGThreads, CTAS)
 grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -100,9 +104,9 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
     volatile int* abort_flag = &ctl->abort_flag;
     const int warp = warp_id(), lane = lane_id();
     const int tiles = p.side[0].tiles + p.side[1].tiles;
-    const int ncols = p.chunk * p.nc;  // accumulator columns
+    const int ncols = CHUNK * p.nc;  // accumulator columns
     const int buf_cols = ncols <= 16 ? 16 : (ncols <= 32 ? 32 : (ncols <= 64 ? 64 : (ncols <= 128 ? 128 : 256)));
-    const uint32_t piece_bytes = static_cast<uint32_t>(p.chunk) * kGK * 2;
+    constexpr uint32_t piece_bytes = CHUNK * kGK * 2;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -138,27 +142,21 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
 
     // The list runs chunk by chunk through all adapters' blocks, so that blocks that have
     // to be gathered (3x a copied one's time) fall to all CTAs alike.
+    // (the epilogue's walk, an item a step)
     auto start = [&]() {
-        GradWalk w{0, 0, 0, 0, 0, lo};
+        GradWalk w{0, 0, 0, 0, lo};
         if (lo < hi) {
             w.tile = static_cast<int>(lo / nblocks);
             const int in = static_cast<int>(lo - static_cast<int64_t>(w.tile) * nblocks);
-            int x = 0, y = p.plan.L - 1;  // the last adapter whose blocks begin at or before it
-            while (x < y) {
-                const int mid = (x + y + 1) >> 1;
-                if (p.plan.boff[mid] <= in) x = mid; else y = mid - 1;
-            }
-            w.a = x;
-            w.b = in - p.plan.boff[x];
-            w.nb = p.plan.boff[x + 1] - p.plan.boff[x];
-            w.t0 = p.plan.toff[x];
+            w.a = p.plan.block[in].x;
+            w.b = in - p.plan.boff[w.a];
+            w.nb = p.plan.boff[w.a + 1] - p.plan.boff[w.a];
         }
         return w;
     };
-    // to the next block; true if it begins another item
-    auto step = [&](GradWalk& w) {
-        if (++w.at >= hi) return true;
-        if (++w.b < w.nb) return false;
+    auto next_item = [&](GradWalk& w) {  // past the last block of the item that is this CTA's
+        w.at += w.nb - w.b;
+        if (w.at >= hi) return;
         w.b = 0;
         do {
             if (++w.a == p.plan.L) {
@@ -167,13 +165,8 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
             }
             w.nb = p.plan.boff[w.a + 1] - p.plan.boff[w.a];
         } while (w.nb == 0);
-        w.t0 = p.plan.toff[w.a];
-        return true;
     };
-    auto rows_of = [&](const GradWalk& w) { return p.plan.tile[w.t0 + w.b / 2]; };
-    // 64 whole rows, neighbours in memory (block b is half b & 1 of tile b / 2)
-    static_assert(kTileRows == 2 * kGK, "two blocks a tile");
-    auto by_tma = [&](const int4& t, int b) { return t.w >= 0 && t.z >= ((b & 1) + 1) * kGK; };
+    auto by_tma = [&](const int4& e) { return e.w >= 0 && (e.z & (kLastBlock - 1)) == kGK; };
 
     if (warp == 0) {
         // --------------------------------------------------- TMA producer --
@@ -181,28 +174,31 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
             int stage = 0;
             uint32_t phase = 0;
             int64_t issued = 0;
-            GradWalk w = start();
-            int4 t = w.at < hi ? rows_of(w) : make_int4(0, 0, 0, 0);
-            while (w.at < hi) {
-                const int sd = w.tile < p.side[0].tiles ? 0 : 1;
-                const int col0 = (sd == 0 ? w.tile : w.tile - p.side[0].tiles) * kGM;
-                const bool tma = by_tma(t, w.b);
-                const int32_t row = t.w + (w.b & 1) * kGK;
-                step(w);
-                if (w.at < hi) t = rows_of(w);  // the next block's, on its way while this one waits
+            int tile = lo < hi ? static_cast<int>(lo / nblocks) : 0;
+            int in = static_cast<int>(lo - static_cast<int64_t>(tile) * nblocks);
+            int4 next = lo < hi ? p.plan.block[in] : make_int4(0, 0, 0, 0);
+            for (int64_t at = lo; at < hi; ++at) {
+                const int4 e = next;
+                const int t = tile;
+                if (++in == nblocks) { in = 0; ++tile; }
+                next = p.plan.block[in];  // on its way while this one waits
+                const int sd = t < p.side[0].tiles ? 0 : 1;
+                const int col0 = (sd == 0 ? t : t - p.side[0].tiles) * kGM;
+                const int parts = sd == 0 ? p.side[0].parts : p.side[1].parts;
                 if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) break;
                 uint64_t* bar = &ctl->full[stage];
-                ctl->gathered[stage] = !tma;
+                const bool tma = by_tma(e);
+                ctl->kind[stage] = (tma ? 0 : kGathered) | ((e.z & kLastBlock) || at + 1 == hi ? kItemEnd : 0) |
+                                   (parts == 2 ? kTwoParts : 0);
                 if (tma) {
-                    const int parts = sd == 0 ? p.side[0].parts : p.side[1].parts;
                     uint8_t* s = ring + stage * p.stage_bytes;
                     mbar_arrive_expect_tx(bar, kGWide + piece_bytes * (p.nc * parts));
-                    tma_load_2d(s, &maps.wide[sd], bar, col0, row);
-                    tma_load_2d(s + kGWide / 2, &maps.wide[sd], bar, col0 + 64, row);
+                    tma_load_2d(s, &maps.wide[sd], bar, col0, e.w);
+                    tma_load_2d(s + kGWide / 2, &maps.wide[sd], bar, col0 + 64, e.w);
                     s += kGWide;
                     for (int part = 0; part < parts; ++part)
                         for (int k = 0; k < p.nc; ++k, s += piece_bytes)
-                            tma_load_2d(s, &maps.narrow[sd == 0 ? part : 2], bar, k * p.chunk, row);
+                            tma_load_2d(s, &maps.narrow[sd == 0 ? part : 2], bar, k * CHUNK, e.w);
                 } else {
                     mbar_arrive(bar);
                 }
@@ -224,34 +220,34 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
             const uint32_t idesc = idesc_bf16_f32_n(kGM, ncols, 1, 1);
             // descriptors of stage 0; an address advances by its bytes / 16
             const uint64_t wide0 = smem_desc(ring0, kGWide / 2, 1024, kLayoutSw128);
-            const uint64_t narrow0 = mnmajor_desc(ring0 + kGWide, 2 * p.chunk, piece_bytes);
-            const uint32_t narrow_step = 2 * p.chunk, part_step = p.nc * piece_bytes / 16;
+            const uint64_t narrow0 = mnmajor_desc(ring0 + kGWide, 2 * CHUNK, piece_bytes);
+            constexpr uint32_t narrow_step = 2 * CHUNK;
+            const uint32_t part_step = p.nc * piece_bytes / 16;
             int stage = 0;
             uint32_t phase = 0, item = 0;
             bool any_mma = false, first = true;
-            for (GradWalk w = start(); w.at < hi;) {
+            for (int64_t at = lo; at < hi; ++at) {
                 const uint32_t buf = item & 1u;
-                const int parts = w.tile < p.side[0].tiles ? p.side[0].parts : p.side[1].parts;
                 if (first && !mbar_wait(&ctl->acc_empty[buf], ((item >> 1) & 1u) ^ 1u, abort_flag, p.status)) break;
                 if (!mbar_wait(&ctl->full[stage], phase, abort_flag, p.status)) break;
                 tc_fence_after();
-                // gathered rows are generic-proxy writes
-                if (*reinterpret_cast<volatile int*>(&ctl->gathered[stage])) fence_proxy_async_smem();
-                const uint32_t at = stage * p.stage_bytes / 16;
+                const int kind = *reinterpret_cast<volatile int*>(&ctl->kind[stage]);
+                if (kind & kGathered) fence_proxy_async_smem();  // gathered rows are generic-proxy writes
+                const uint32_t off = stage * p.stage_bytes / 16;
                 const uint32_t d = tmem + buf * buf_cols;
 #pragma unroll
                 for (int ks = 0; ks < kGK / 16; ++ks)
-                    umma_bf16(d, wide0 + at + ks * 128, narrow0 + at + ks * narrow_step, idesc,
+                    umma_bf16(d, wide0 + off + ks * 128, narrow0 + off + ks * narrow_step, idesc,
                               (!first || ks > 0) ? 1u : 0u);
-                if (parts == 2) {
+                if (kind & kTwoParts) {
 #pragma unroll
                     for (int ks = 0; ks < kGK / 16; ++ks)
-                        umma_bf16(d, wide0 + at + ks * 128, narrow0 + at + part_step + ks * narrow_step, idesc, 1u);
+                        umma_bf16(d, wide0 + off + ks * 128, narrow0 + off + part_step + ks * narrow_step, idesc, 1u);
                 }
                 umma_commit(&ctl->empty[stage]);
                 any_mma = true;
                 if (++stage == p.stages) { stage = 0; phase ^= 1u; }
-                first = step(w);
+                first = (kind & kItemEnd) != 0;
                 if (first) {
                     umma_commit(&ctl->acc_full[buf]);
                     ++item;
@@ -269,95 +265,87 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
         const int gt = threadIdx.x - 64;  // 0 .. 127
         int stage = 0;
         uint32_t phase = 0;
-        // 16 pieces of 8 columns a row of the wide source, 8 rows a step; chunk / 8 of the
-        // narrow one's, 128 / (chunk / 8) rows a step
-        const int pc = gt & 15;
-        const int npc = p.chunk / 8, np = gt % npc, nstep = 128 / npc;
-        // a block's rows of this thread, loaded one block ahead
-        struct Rows {
-            int32_t wide[kGK / 8], narrow[kGK / 16];
-        };
-        auto load_rows = [&](const int4& t, int b, Rows& r) {
-            const int off = (b & 1) * kGK, valid = t.z - off;
+        // wide: 16 pieces of 8 columns a row, 8 rows a step; narrow: CHUNK / 8 pieces a
+        // row, kStep rows a step.  A block's rows are loaded one block ahead, its entry
+        // two.
+        constexpr int kPieces = CHUNK / 8, kStep = 128 / kPieces, kSteps = kGK / kStep < 1 ? 1 : kGK / kStep;
+        const int pc = gt & 15, np = gt % kPieces, nr = gt / kPieces;
+        int32_t wide[kGK / 8], narrow[kSteps];
+        auto load_rows = [&](const int4& e) {
+            const int n = e.z & (kLastBlock - 1);
             auto token = [&](int rr) {  // of the block's row rr
-                return rr >= valid ? -1 : (t.w >= 0 ? t.w + off + rr : p.plan.order[t.y + off + rr]);
+                return rr >= n ? -1 : (e.w >= 0 ? e.w + rr : p.plan.order[e.y + rr]);
             };
 #pragma unroll
-            for (int j = 0; j < kGK / 8; ++j) r.wide[j] = token((gt >> 4) + 8 * j);
+            for (int j = 0; j < kGK / 8; ++j) wide[j] = token((gt >> 4) + 8 * j);
 #pragma unroll
-            for (int j = 0; j < kGK / 16; ++j) {
-                const int rr = gt / npc + nstep * j;
-                r.narrow[j] = rr < kGK ? token(rr) : -1;
-            }
+            for (int j = 0; j < kSteps; ++j) narrow[j] = token(nr + kStep * j);
         };
-        GradWalk w = start();
-        Rows rows;
-        bool tma = true;
-        if (w.at < hi) {
-            const int4 t = rows_of(w);
-            tma = by_tma(t, w.b);
-            if (!tma) load_rows(t, w.b, rows);
+        int tile = lo < hi ? static_cast<int>(lo / nblocks) : 0;
+        int in = static_cast<int>(lo - static_cast<int64_t>(tile) * nblocks);
+        int4 e = make_int4(0, 0, 0, 0), next = e;
+        if (lo < hi) {
+            e = p.plan.block[in];
+            if (!by_tma(e)) load_rows(e);
+            next = p.plan.block[in + 1 == nblocks ? 0 : in + 1];
         }
-        while (w.at < hi) {
-            const bool now_tma = tma;
-            const Rows now = rows;
-            const int sd = w.tile < p.side[0].tiles ? 0 : 1;
-            const int col0 = (sd == 0 ? w.tile : w.tile - p.side[0].tiles) * kGM;
-            step(w);
-            if (w.at < hi) {
-                const int4 t = rows_of(w);
-                tma = by_tma(t, w.b);
-                if (!tma) load_rows(t, w.b, rows);
-            }
+        // swizzled places of this thread's pieces: 16-byte piece index XOR the address bits
+        // 7 and up, as TMA does (narrow rows are 2 CHUNK bytes)
+        const uint32_t wide_to = (pc >> 3) * (kGWide / 2) + (gt >> 4) * 128 + (((pc & 7) ^ ((gt >> 4) & 7)) << 4);
+        for (int64_t at = lo; at < hi; ++at) {
+            const bool tma = by_tma(e);
+            const int t = tile;
             if (!warp_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status, 32)) break;
-            if (now_tma) {
+            if (tma) {
                 mbar_arrive(&ctl->full[stage]);
             } else {
-                const GradSide& side = p.side[sd];
+                const int sd = t < p.side[0].tiles ? 0 : 1;
+                const int col = (sd == 0 ? t : t - p.side[0].tiles) * kGM + pc * 8;
+                const uint16_t* src = sd == 0 ? p.side[0].wide : p.side[1].wide;
+                const int cols = sd == 0 ? p.side[0].cols : p.side[1].cols;
                 const uint32_t s = ring0 + stage * p.stage_bytes;
-                const bool in = col0 + pc * 8 < side.cols;
+                const bool inside = col < cols;
+                src += inside ? col : 0;
 #pragma unroll
-                for (int j = 0; j < kGK / 8; ++j) {
-                    const int rr = (gt >> 4) + 8 * j;
-                    const bool v = in && now.wide[j] >= 0;
-                    cp_async_16(s + (pc >> 3) * (kGWide / 2) + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4),
-                                v ? side.wide + static_cast<int64_t>(now.wide[j]) * side.cols + col0 + pc * 8 : side.wide,
-                                v ? 16u : 0u);
-                }
-                // swizzled over the row's width as TMA does (16-byte piece index XOR address
-                // bits 7 and up)
+                for (int j = 0; j < kGK / 8; ++j)
+                    cp_async_16(s + wide_to + j * 1024, src + static_cast<int64_t>(max(wide[j], 0)) * cols,
+                                inside && wide[j] >= 0 ? 16u : 0u);
+                const int parts = sd == 0 ? p.side[0].parts : p.side[1].parts;
+                for (int part = 0; part < parts; ++part) {
+                    const uint16_t* nsrc = sd == 1 ? p.side[1].narrow[0] : (part == 0 ? p.side[0].narrow[0] : p.side[0].narrow[1]);
+                    for (int k = 0; k < p.nc; ++k) {
+                        const int c = k * CHUNK + np * 8;
+                        const uint32_t to = s + kGWide + (part * p.nc + k) * piece_bytes;
 #pragma unroll
-                for (int j = 0; j < kGK / 16; ++j) {
-                    const int rr = gt / npc + nstep * j;
-                    if (rr >= kGK) break;
-                    const uint32_t flip = static_cast<uint32_t>((rr * p.chunk * 2) >> 7) & (npc - 1);
-                    uint32_t to = s + kGWide + rr * p.chunk * 2 + ((np ^ flip) << 4);
-                    for (int part = 0; part < side.parts; ++part)
-                        for (int k = 0; k < p.nc; ++k, to += piece_bytes) {
-                            const int c = k * p.chunk + np * 8;
-                            const uint16_t* src = side.narrow[part];
-                            const bool v = now.narrow[j] >= 0 && c < p.r;
-                            cp_async_16(to, v ? src + static_cast<int64_t>(now.narrow[j]) * p.r + c : src, v ? 16u : 0u);
+                        for (int j = 0; j < kSteps; ++j) {
+                            const int rr = nr + kStep * j;
+                            const uint32_t flip = static_cast<uint32_t>((rr * CHUNK * 2) >> 7) & (kPieces - 1);
+                            if (kStep <= kGK || rr < kGK)
+                                cp_async_16(to + rr * CHUNK * 2 + ((np ^ flip) << 4),
+                                            nsrc + static_cast<int64_t>(max(narrow[j], 0)) * p.r + (c < p.r ? c : 0),
+                                            narrow[j] >= 0 && c < p.r ? 16u : 0u);
                         }
+                    }
                 }
                 cp_async_mbar_arrive(&ctl->full[stage]);
             }
             if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+            if (++in == nblocks) { in = 0; ++tile; }
+            e = next;
+            if (at + 1 < hi && !by_tma(e)) load_rows(e);
+            next = p.plan.block[in + 1 == nblocks ? 0 : in + 1];
         }
         cp_async_wait<0>();
     } else {
         // ------------------------------------------------------- epilogue --
         const int q = warp & 3, row = q * 32 + lane;  // this thread's wide column
         uint32_t item = 0;
-        for (GradWalk w = start(); w.at < hi; ++item) {
+        for (GradWalk w = start(); w.at < hi; next_item(w), ++item) {
             const uint32_t buf = item & 1u;
             // the item, and the CTAs that hold its blocks
             const int a = w.a, tile = w.tile;
             const int64_t i_lo = w.at - w.b, i_hi = i_lo + w.nb;
             const int64_t c_lo = ((i_lo + 1) * G - 1) / total, c_hi = (i_hi * G - 1) / total;
-            w.at = i_hi - 1 < hi ? i_hi - 1 : hi - 1;
-            w.b = w.nb - 1;
-            step(w);
             const int sd = tile < p.side[0].tiles ? 0 : 1;
             const GradSide& side = p.side[sd];
             const int col = (sd == 0 ? tile : tile - p.side[0].tiles) * kGM + row;
@@ -449,7 +437,7 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
     }
 }
 
-template <int RING, int CTAS>
+template <int RING, int CTAS, int CHUNK>
 int launch_grad(const GradMaps& m, GradParams p, cudaStream_t st) {
     constexpr size_t smem = 1024 + RING;
     int dev = 0;
@@ -458,7 +446,7 @@ int launch_grad(const GradMaps& m, GradParams p, cudaStream_t st) {
     if (dev < 0 || dev >= 64) dev = 0;
     static std::atomic<bool> smem_set[64];
     if (!smem_set[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(grad_kernel<RING, CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(grad_kernel<RING, CTAS, CHUNK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(smem));
         if (e != cudaSuccess) { record_cuda_error(e); return GG_ERR_CUDA; }
         smem_set[dev].store(true, std::memory_order_release);
@@ -467,13 +455,12 @@ int launch_grad(const GradMaps& m, GradParams p, cudaStream_t st) {
     if (p.stages > kGMaxStages) p.stages = kGMaxStages;
     // every CTA resident at once, none with less than kGMinBlocks blocks of the
     // blocks there can be
-    const int64_t most = p.plan.T / kGK + (p.plan.T < p.plan.L ? p.plan.T : p.plan.L);
-    int64_t G = most * (p.side[0].tiles + p.side[1].tiles) / kGMinBlocks;
+    int64_t G = p.plan.max_blocks * (p.side[0].tiles + p.side[1].tiles) / kGMinBlocks;
     if (G > int64_t(CTAS) * num_sms()) G = int64_t(CTAS) * num_sms();
     if (G > kGradCtas) G = kGradCtas;
     if (G < 1) G = 1;
     clear_pending_launch_error();
-    grad_kernel<RING, CTAS><<<static_cast<unsigned>(G), kGThreads, smem, st>>>(m, p);
+    grad_kernel<RING, CTAS, CHUNK><<<static_cast<unsigned>(G), kGThreads, smem, st>>>(m, p);
     return launch_result();
 }
 
@@ -485,8 +472,8 @@ int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, c
     GradParams p{};
     p.plan = plan;
     p.r = r;
-    p.chunk = rank_pad(r);
-    p.nc = (r + p.chunk - 1) / p.chunk;
+    const int chunk = rank_pad(r);
+    p.nc = (r + chunk - 1) / chunk;
     p.counter = counters;
     p.sums = sums;
     p.status = status;
@@ -494,19 +481,21 @@ int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, c
         p.side[0] = GradSide{X, {V, V_lo}, 2, static_cast<int>(K), static_cast<int>((K + kGM - 1) / kGM), dA};
     if (dB)
         p.side[1] = GradSide{dY, {U, nullptr}, 1, static_cast<int>(N), static_cast<int>((N + kGM - 1) / kGM), dB};
-    p.stage_bytes = kGWide + p.chunk * kGK * 2 * p.nc * (dA ? 2 : 1);
+    p.stage_bytes = kGWide + chunk * kGK * 2 * p.nc * (dA ? 2 : 1);
     GradMaps m{};
     if (dA) {
         if (!encode_map_2d(&m.wide[0], X, K, plan.T, K, 64, kGK)) return GG_ERR_CUDA;
-        if (!encode_map_2d(&m.narrow[0], V, r, plan.T, r, p.chunk, kGK)) return GG_ERR_CUDA;
-        if (!encode_map_2d(&m.narrow[1], V_lo, r, plan.T, r, p.chunk, kGK)) return GG_ERR_CUDA;
+        if (!encode_map_2d(&m.narrow[0], V, r, plan.T, r, chunk, kGK)) return GG_ERR_CUDA;
+        if (!encode_map_2d(&m.narrow[1], V_lo, r, plan.T, r, chunk, kGK)) return GG_ERR_CUDA;
     }
     if (dB) {
         if (!encode_map_2d(&m.wide[1], dY, N, plan.T, N, 64, kGK)) return GG_ERR_CUDA;
-        if (!encode_map_2d(&m.narrow[2], U, r, plan.T, r, p.chunk, kGK)) return GG_ERR_CUDA;
+        if (!encode_map_2d(&m.narrow[2], U, r, plan.T, r, chunk, kGK)) return GG_ERR_CUDA;
     }
     // two CTAs an SM for ranks up to 64, one above
-    return p.nc == 1 ? launch_grad<98304, 2>(m, p, st) : launch_grad<196608, 1>(m, p, st);
+    if (chunk == 16) return launch_grad<98304, 2, 16>(m, p, st);
+    if (chunk == 32) return launch_grad<98304, 2, 32>(m, p, st);
+    return p.nc == 1 ? launch_grad<98304, 2, 64>(m, p, st) : launch_grad<196608, 1, 64>(m, p, st);
 }
 
 }  // namespace gg

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(32) plan_scan_kernel(PlanView v) {
     for (int a0 = 0; a0 < v.L; a0 += 32) {
         const int a = a0 + lane;
         const int c = a < v.L ? v.goff[a + 1] : 0;
-        int x = c, y = (c + kTileRows - 1) / kTileRows, z = (c + 63) / 64;
+        int x = c, y = (c + kTileRows - 1) / kTileRows, z = (c + kBlockRows - 1) / kBlockRows;
         for (int d = 1; d < 32; d <<= 1) {
             const int xs = __shfl_up_sync(0xffffffffu, x, d), ys = __shfl_up_sync(0xffffffffu, y, d);
             const int zs = __shfl_up_sync(0xffffffffu, z, d);
@@ -140,19 +140,23 @@ __global__ void __launch_bounds__(kUnit) plan_order_kernel(PlanView v) {
     }
 }
 
-// The row tiles, a thread each: its adapter by bisection of the tile offsets.
+// The row tiles and blocks, a thread each: its adapter by bisection of the offsets.
 __global__ void __launch_bounds__(128) plan_tiles_kernel(PlanView v) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
-    if (i >= *v.ntile) return;
-    int lo = 0, hi = v.L - 1;  // the last adapter whose first tile is not past i
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (v.toff[mid] <= i) lo = mid; else hi = mid - 1;
-    }
-    const int at = v.goff[lo] + static_cast<int>(i - v.toff[lo]) * kTileRows;
-    const int n = min(kTileRows, v.goff[lo + 1] - at);
-    const int first = v.order[at];
-    v.tile[i] = make_int4(lo, at, n, v.order[at + n - 1] - first == n - 1 ? first : -1);
+    auto entry = [&](const int32_t* off, int rows, bool mark_last) {
+        int lo = 0, hi = v.L - 1;  // the last adapter whose first entry is not past i
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (off[mid] <= i) lo = mid; else hi = mid - 1;
+        }
+        const int at = v.goff[lo] + static_cast<int>(i - off[lo]) * rows;
+        const int left = v.goff[lo + 1] - at, n = min(rows, left);
+        const int first = v.order[at];
+        return make_int4(lo, at, n + (mark_last && left <= rows ? kLastBlock : 0),
+                         v.order[at + n - 1] - first == n - 1 ? first : -1);
+    };
+    if (i < v.toff[v.L]) v.tile[i] = entry(v.toff, kTileRows, false);
+    if (i < v.boff[v.L]) v.block[i] = entry(v.boff, kBlockRows, true);
 }
 
 }  // namespace
@@ -163,7 +167,7 @@ int lora_plan_launch(const int32_t* ids, const PlanView& v, int32_t* status, cud
     plan_groups_kernel<<<static_cast<unsigned>((v.L + 3) / 4), 128, 0, st>>>(v);
     plan_scan_kernel<<<1, 32, 0, st>>>(v);
     plan_order_kernel<<<static_cast<unsigned>(v.units), kUnit, 0, st>>>(v);
-    plan_tiles_kernel<<<static_cast<unsigned>((v.max_tiles + 127) / 128), 128, 0, st>>>(v);
+    plan_tiles_kernel<<<static_cast<unsigned>((v.max_blocks + 127) / 128), 128, 0, st>>>(v);
     return launch_result();
 }
 
