@@ -118,6 +118,12 @@ SHAPES = [
     (1000, 24, 24, 2, 8, "bare"), (2600, 200, 1032, 5, 16, "runs"), (2600, 1032, 200, 5, 16, "runs"),
     (2570, 1040, 1096, 11, 24, "mixed"), (2816, 1024, 1024, 3, 64, "runs"), (2305, 1032, 1288, 3, 136, "mixed"),
     (2400, 1096, 1032, 70, 8, "mixed"), (2560, 1024, 1024, 2, 256, "runs"),
+    # long reductions of few tiles, split over clusters (forward: K, backward: N)
+    (300, 2640, 136, 3, 24, "mixed"), (300, 136, 2640, 3, 24, "mixed"), (513, 2640, 520, 5, 136, "runs"),
+    (513, 520, 2640, 5, 136, "runs"),
+    # more pair tiles than a round of the GPU holds
+    (2600, 264, 2056, 4, 24, "runs"), (2600, 136, 1800, 6, 72, "mixed"), (2600, 2056, 264, 4, 24, "runs"),
+    (2600, 1800, 136, 6, 72, "mixed"), (2560, 200, 4856, 3, 8, "runs"), (2560, 4856, 200, 3, 8, "runs"),
 ]
 
 

@@ -250,6 +250,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * kPN;
 #pragma unroll 1
             for (int c = 0; c < kPN; c += 128) {
+                __syncwarp();
                 uint32_t v[4][32];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(ta + c + 32 * k, v[k]);

@@ -290,11 +290,13 @@ int launch_project(const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap
     int room[kMaxCluster + 1];
     const int rc = rooms.get(project_kernel<B_MN>, kProjectSmem, room);
     if (rc != GG_OK) return rc;
-    // the widest split whose clusters are all resident at once
+    // The widest split whose clusters are resident at once with an eighth to spare: the
+    // low-rank product may still hold some SMs, and a cluster that starts late runs
+    // alone (300 rows of 4096 x 4096: 29 us at 96 of 97 clusters of 3, 25 in clusters of 2).
     const int64_t nb = (p.Kred + kRK - 1) / kRK;
     const int64_t tiles = static_cast<int64_t>(p.mtiles) * ((p.ncols + kRN - 1) / kRN);
     int S = kMaxCluster;
-    while (S > 1 && (tiles > room[S] || S > nb)) --S;
+    while (S > 1 && (tiles * 8 > room[S] * 7 || S > nb)) --S;
     if (tiles * S >= (int64_t(1) << 31)) return GG_ERR_UNSUPPORTED;
     ClusterLaunch l(tiles * S, kRThreads, kProjectSmem, S, true, st);
     clear_pending_launch_error();
