@@ -118,6 +118,8 @@ SHAPES = [
     (1000, 24, 24, 2, 8, "bare"), (2600, 200, 1032, 5, 16, "runs"), (2600, 1032, 200, 5, 16, "runs"),
     (2570, 1040, 1096, 11, 24, "mixed"), (2816, 1024, 1024, 3, 64, "runs"), (2305, 1032, 1288, 3, 136, "mixed"),
     (2400, 1096, 1032, 70, 8, "mixed"), (2560, 1024, 1024, 2, 256, "runs"),
+    # as many adapters as there may be, in one unit's plan and in several
+    (256, 64, 72, 2048, 8, "mixed"), (600, 72, 64, 2048, 8, "mixed"),
     # long reductions of few tiles, split over clusters (forward: K, backward: N)
     (300, 2640, 136, 3, 24, "mixed"), (300, 136, 2640, 3, 24, "mixed"), (513, 2640, 520, 5, 136, "runs"),
     (513, 520, 2640, 5, 136, "runs"),

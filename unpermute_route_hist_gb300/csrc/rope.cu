@@ -24,7 +24,7 @@ int num_sms();
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;  // 52 us against 54 with 256 on 16384 tokens of 40 heads, 28 against 30 out of place
 constexpr int kRopeMaxTokens = 8;    // of a CTA
 constexpr int kRopeMaxRot = 1024;
 
