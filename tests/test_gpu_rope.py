@@ -177,6 +177,8 @@ def test_empty_and_refusals(gg):
         gg.rope(q.transpose(1, 2).contiguous().transpose(1, 2), None, pos, freqs)
     with pytest.raises(ValueError):
         gg.rope(q, None, pos, freqs, out_q=q[:, :1])
+    with pytest.raises(ValueError):
+        gg.rope(q, None, pos, gg.rope_freqs(64, device="cpu"))
     big = gg.rope_freqs(2048, device=dev())
     with pytest.raises(gg.GGError):
         gg.rope(torch.zeros(1, 1, 2048, dtype=torch.bfloat16, device=dev()), None, pos[:1], big)

@@ -440,6 +440,8 @@ def _rope(q, k, positions, freqs, interleaved, out_q, out_k, backward):
     rot, axes = freqs.rot_dim, freqs.axes
     if rot > D:
         raise ValueError("freqs turn %d elements of a head of %d" % (rot, D))
+    if not freqs.steps.is_cuda:
+        raise ValueError("freqs must be on the GPU")
     want = (T,) if axes == 1 and positions.dim() == 1 else (axes, T)
     if positions.dtype is not torch.int32 or positions.shape != want or not positions.is_cuda or \
             not positions.is_contiguous():
