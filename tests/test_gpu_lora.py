@@ -246,6 +246,48 @@ def test_graph_capture(gg):
     assert torch.equal(Y, want)
 
 
+def test_offsets_past_32_bits(gg):
+    """270000 tokens of width 8192: elements past 2^31 of X, Y, dY and dX.  The last 70
+    tokens have an adapter of their own, so its gradients are theirs alone."""
+    T, W, r, last = 270000, 8192, 8, 70
+    g = torch.Generator(device=dev()).manual_seed(1)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=dev(), dtype=torch.bfloat16)
+    ids = torch.zeros(T, dtype=torch.int32, device=dev())
+    ids[-last:] = 1
+    plan, scale = gg.lora_plan(ids, 2), torch.tensor([1.0, 0.5], device=dev())
+    cpu = lambda t: t.double().cpu().numpy()
+    big = rnd(T, W)
+    tail = cpu(big[-last:])
+    # wide input: X past 2^31, then dX and dA
+    d = dict(X=tail, W=cpu(rnd(16, W)), A=cpu(rnd(2, r, W) * 0.01), B=cpu(rnd(2, 16, r)), dY=cpu(rnd(T, 16)[-last:]))
+    d["ids"], d["scale"] = np.ones(last, np.int32), np.array([1.0, 0.5], np.float32)
+    dY = torch.zeros(T, 16, dtype=torch.bfloat16, device=dev())
+    dY[-last:] = put(d["dY"])
+    ops = [put(d[k]) for k in ("W", "A", "B")]
+    Y, U = gg.lora_forward(big, *ops, scale, plan)
+    ref = forward_ref(d)
+    within(U[-last:], ref[1], ref[3] * 8, "U")      # sums of 8192 terms: 8 times the bound's 1024
+    within(Y[-last:], ref[0], ref[2] * 8, "Y")
+    dX, dA, _ = gg.lora_backward(dY, big, *ops, scale, plan, U, want=(True, True, False))
+    ref = backward_ref(d, get(U[-last:]))
+    within(dX[-last:], ref[0], ref[3], "dX")
+    within(dA[1:], ref[1][1:], ref[4][1:] , "dA")
+    assert not get(dX[:1000]).any()
+    del dX
+    # wide output: Y and dY past 2^31, then dB
+    d = dict(X=cpu(rnd(T, 16)[-last:]), W=cpu(rnd(W, 16)), A=cpu(rnd(2, r, 16)), B=cpu(rnd(2, W, r) * 0.1), dY=tail,
+             ids=d["ids"], scale=d["scale"])
+    X = torch.zeros(T, 16, dtype=torch.bfloat16, device=dev())
+    X[-last:] = put(d["X"])
+    ops = [put(d[k]) for k in ("W", "A", "B")]
+    Y, U = gg.lora_forward(X, *ops, scale, plan)
+    ref = forward_ref(d)
+    within(Y[-last:], ref[0], ref[2], "Y, wide")
+    dB = gg.lora_backward(big, X, *ops, scale, plan, U, want=(False, False, True))[2]
+    ref = backward_ref(d, get(U[-last:]))
+    within(dB[1:], ref[2][1:], ref[5][1:], "dB")
+
+
 def test_scale_none_and_wanted_gradients(gg):
     d = make(130, 128, 136, 3, 16, "mixed", seed=10)
     d["scale"][:] = 1.0

@@ -157,6 +157,19 @@ def test_infinities_stay_in_their_pair(gg):
     assert torch.equal(got[same], want[same]) and not torch.isfinite(got[4, 1, 5])
 
 
+def test_offsets_past_32_bits(gg):
+    """Heads whose elements lie past 2^31 of their tensor, in place on a strided view."""
+    T, H, D = 270000, 64, 128
+    buf = torch.randn(T, H, D, dtype=torch.bfloat16, device=dev())
+    freqs = gg.rope_freqs(D, device=dev())
+    pos = torch.arange(T, dtype=torch.int32, device=dev())
+    want, _ = gg.rope(buf[-5:, :63].contiguous(), None, pos[-5:], freqs)
+    keep = buf[-5:, 63].clone()
+    q = buf[:, :63]
+    gg.rope(q, None, pos, freqs, out_q=q)
+    assert torch.equal(q[-5:], want) and torch.equal(buf[-5:, 63], keep)
+
+
 def test_empty_and_refusals(gg):
     freqs = gg.rope_freqs(64, device=dev())
     pos = torch.zeros(4, dtype=torch.int32, device=dev())

@@ -122,38 +122,53 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                 const int32_t nh = ti.n0 + static_cast<int32_t>(rank) * (kPN / 2);
                 const int ne = p.plan.cnt[ti.unit];
                 const int32_t* gid = p.plan.gid + ti.unit * p.plan.slots;
-                const int total = nb + ext_blocks(ne);
-                for (int i = 0; i < total; ++i) {
+                for (int i = 0; i < nb; ++i) {
                     if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
                     uint8_t* sA = ring + stage * kPStage;
                     uint8_t* sB = sA + kPSlot;
                     const uint32_t bar = mapa_u32(&ctl->full[stage], 0);
-                    if (i < nb) {
-                        const int32_t red = i * kPK;
-                        if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2 * kPStage);
-                        tma_load_2d_pair(sA, &tmX, bar, red, arow);
-                        if (B_MN) {
-                            tma_load_2d_pair(sB, &tmW, bar, nh, red);
-                            tma_load_2d_pair(sB + 8192, &tmW, bar, nh + 64, red);
-                        } else {
-                            tma_load_2d_pair(sB, &tmW, bar, red, nh);
-                        }
+                    const int32_t red = i * kPK;
+                    if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2 * kPStage);
+                    tma_load_2d_pair(sA, &tmX, bar, red, arow);
+                    if (B_MN) {
+                        tma_load_2d_pair(sB, &tmW, bar, nh, red);
+                        tma_load_2d_pair(sB + 8192, &tmW, bar, nh + 64, red);
                     } else {
-                        if (!waited) { pdl_wait(); waited = true; }  // U (V) of the kernel before
-                        const int xi = i - nb;
-                        const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
-                        const int en = p.r <= 64 ? min(p.epb, ne - ef) : 1;
-                        const int rc = p.r <= 64 ? 0 : (xi % rchunks) * 64;
-                        if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2u * (eb + eb * en));
-                        tma_load_2d_pair(sA, &tmU, bar, rc, arow);
-                        for (int e = 0; e < en; ++e) {
-                            const int g = gid[ef + e];
-                            if (B_MN) {
-                                tma_load_3d_pair(sB + e * eb, &tmE, bar, nh, rc, g);
-                                tma_load_3d_pair(sB + e * eb + eb / 2, &tmE, bar, nh + 64, rc, g);
-                            } else {
-                                tma_load_3d_pair(sB + e * eb, &tmE, bar, rc, nh, g);
-                            }
+                        tma_load_2d_pair(sB, &tmW, bar, red, nh);
+                    }
+                    ++issued;
+                    if (++stage == kPStages) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                const int xb = ext_blocks(ne);
+                int32_t g[4] = {0, 0, 0, 0};  // a block's adapters, loaded one block ahead
+                auto load_ids = [&](int xi) {
+                    const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e < p.epb && ef + e < ne) g[e] = gid[ef + e];
+                };
+                if (xb > 0) load_ids(0);
+                for (int xi = 0; xi < xb; ++xi) {
+                    const int en = p.r <= 64 ? min(p.epb, ne - xi * p.epb) : 1;
+                    const int rc = p.r <= 64 ? 0 : (xi % rchunks) * 64;
+                    const int32_t now[4] = {g[0], g[1], g[2], g[3]};
+                    if (xi + 1 < xb) load_ids(xi + 1);
+                    if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+                    if (!waited) { pdl_wait(); waited = true; }  // U (V) of the kernel before
+                    uint8_t* sA = ring + stage * kPStage;
+                    uint8_t* sB = sA + kPSlot;
+                    const uint32_t bar = mapa_u32(&ctl->full[stage], 0);
+                    if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2u * (eb + eb * en));
+                    tma_load_2d_pair(sA, &tmU, bar, rc, arow);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (e >= en) break;
+                        if (B_MN) {
+                            tma_load_3d_pair(sB + e * eb, &tmE, bar, nh, rc, now[e]);
+                            tma_load_3d_pair(sB + e * eb + eb / 2, &tmE, bar, nh + 64, rc, now[e]);
+                        } else {
+                            tma_load_3d_pair(sB + e * eb, &tmE, bar, rc, nh, now[e]);
                         }
                     }
                     ++issued;
@@ -181,7 +196,20 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             for (int64_t t = slot; t < p.tiles && ok; t += nslot, ++acc) {
                 const PairTile ti = pair_tile(t, p);
                 const int ne = p.plan.cnt[ti.unit];
-                const uint32_t* masks = p.plan.mask + ti.unit * p.plan.slots * kUnitWords;
+                const uint4* masks = reinterpret_cast<const uint4*>(p.plan.mask + ti.unit * p.plan.slots * kUnitWords);
+                // the rows of a block's adapters, loaded one block ahead (the first tile's
+                // with its shared blocks still to come)
+                uint4 m[4][2];
+                auto load_masks = [&](int xi) {
+                    const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (e >= p.epb || ef + e >= ne) continue;
+                        m[e][0] = __ldg(masks + 2 * (ef + e));
+                        m[e][1] = __ldg(masks + 2 * (ef + e) + 1);
+                    }
+                };
+                load_masks(0);
                 const uint32_t buf = acc & 1u;
                 if (!mbar_wait(&ctl->tmem_empty[buf], ((acc >> 1) & 1u) ^ 1u, abort_flag, p.status, 0, kWaitLimitNs,
                                true))
@@ -205,17 +233,17 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                 }
                 const int xb = ext_blocks(ne);
                 for (int xi = 0; xi < xb && ok; ++xi) {
-                    const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
-                    const int en = p.r <= 64 ? min(p.epb, ne - ef) : 1;
+                    const int en = p.r <= 64 ? min(p.epb, ne - xi * p.epb) : 1;
                     const int left = p.r <= 64 ? p.r : min(64, p.r - (xi % rchunks) * 64);
-                    const uint32_t eb = 256u * p.rpad;
                     if (!mbar_wait(&ctl->full[stage], phase, abort_flag, p.status)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t sA = ring0 + stage * kPStage, sB = sA + kPSlot;
-                    for (int e = 0; e < en; ++e) {
-                        const uint4 m0 = __ldg(reinterpret_cast<const uint4*>(masks + (ef + e) * kUnitWords));
-                        const uint4 m1 = __ldg(reinterpret_cast<const uint4*>(masks + (ef + e) * kUnitWords) + 1);
-                        const uint32_t keep[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+                    const uint32_t eb = 256u * p.rpad;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (e >= en) break;
+                        const uint32_t keep[8] = {m[e][0].x, m[e][0].y, m[e][0].z, m[e][0].w,
+                                                  m[e][1].x, m[e][1].y, m[e][1].z, m[e][1].w};
                         for (int ks = 0; ks < (left + 15) / 16; ++ks) {
                             const uint64_t ad = kmajor_desc(sA + ks * 32, p.rpad * 2);
                             const uint64_t bd = B_MN ? smem_desc(sB + e * eb + ks * 2048, eb / 2, 1024, kLayoutSw128)
@@ -224,6 +252,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                         }
                     }
                     umma_commit_pair(&ctl->empty[stage], 0x3);
+                    if (xi + 1 < xb) load_masks(xi + 1);
                     if (++stage == kPStages) { stage = 0; phase ^= 1u; }
                 }
                 if (ok) umma_commit_pair(&ctl->tmem_full[buf], 0x3);
