@@ -338,48 +338,63 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
         cp_async_wait<0>();
     } else {
         // ------------------------------------------------------- epilogue --
+        constexpr int kCols = 16;  // rank columns a step
         const int q = warp & 3, row = q * 32 + lane;  // this thread's wide column
         uint32_t item = 0;
-        for (GradWalk w = start(); w.at < hi; next_item(w), ++item) {
-            const uint32_t buf = item & 1u;
-            // the item, and the CTAs that hold its blocks
+        GradWalk w = start();
+        while (w.at < hi) {
+            const uint32_t buf = item & 1u, round = (item >> 1) & 1u;
+            ++item;
+            // the item, and (if it is not all this CTA's) the CTAs that hold its blocks
             const int a = w.a, tile = w.tile;
             const int64_t i_lo = w.at - w.b, i_hi = i_lo + w.nb;
-            const int64_t c_lo = ((i_lo + 1) * G - 1) / total, c_hi = (i_hi * G - 1) / total;
+            int64_t c_lo = blockIdx.x, c_hi = blockIdx.x;
+            if (i_lo < lo || i_hi > hi) {
+                c_lo = ((i_lo + 1) * G - 1) / total;
+                c_hi = (i_hi * G - 1) / total;
+            }
+            next_item(w);  // (its loads before the wait)
             const int sd = tile < p.side[0].tiles ? 0 : 1;
             const GradSide& side = p.side[sd];
             const int col = (sd == 0 ? tile : tile - p.side[0].tiles) * kGM + row;
-            // eight rank columns of this wide column to the gradient
-            auto store = [&](int c, const float (&v)[8]) {
+            // kCols rank columns of this wide column to the gradient
+            auto store = [&](int c0, const float (&v)[kCols]) {
                 if (col >= side.cols) return;
-                if (sd == 0) {
-                    uint16_t* o = side.out + (static_cast<int64_t>(a) * p.r + c) * side.cols + col;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        reinterpret_cast<__nv_bfloat16*>(o)[static_cast<int64_t>(k) * side.cols] = __float2bfloat16(v[k]);
-                } else {
-                    *reinterpret_cast<uint4*>(side.out + (static_cast<int64_t>(a) * side.cols + col) * p.r + c) =
-                        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                   pack_bf16x2(v[6], v[7]));
+                for (int g = 0; g < kCols; g += 8) {
+                    const int c = c0 + g;
+                    if (c >= p.r) break;
+                    if (sd == 0) {
+                        uint16_t* o = side.out + (static_cast<int64_t>(a) * p.r + c) * side.cols + col;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            reinterpret_cast<__nv_bfloat16*>(o)[static_cast<int64_t>(k) * side.cols] = __float2bfloat16(v[g + k]);
+                    } else {
+                        *reinterpret_cast<uint4*>(side.out + (static_cast<int64_t>(a) * side.cols + col) * p.r + c) =
+                            make_uint4(pack_bf16x2(v[g], v[g + 1]), pack_bf16x2(v[g + 2], v[g + 3]),
+                                       pack_bf16x2(v[g + 4], v[g + 5]), pack_bf16x2(v[g + 6], v[g + 7]));
+                    }
                 }
             };
             const size_t slot = static_cast<size_t>(kGM) * p.r;
             // slot 1 of the CTA an item begins in, slot 0 of those it goes on in
             float* mine = c_lo == c_hi ? nullptr : p.sums + (2 * blockIdx.x + (blockIdx.x == c_lo ? 1 : 0)) * slot + row;
             // the four warps go on, or give up, together
-            const bool ok = warp_wait(&ctl->acc_full[buf], (item >> 1) & 1u, abort_flag, p.status, 64);
+            const bool ok = warp_wait(&ctl->acc_full[buf], round, abort_flag, p.status, 64);
             if (!all_of_128(ok)) break;
             tc_fence_after();
-            for (int c = 0; c < p.r; c += 8) {
-                uint32_t u[8];
-                tmem_ld_32x32b_x8(tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * buf_cols + c, u);
+            for (int c = 0; c < p.r; c += kCols) {
+                uint32_t u[kCols];
+                const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * buf_cols + c;
+                tmem_ld_32x32b_x16(ta, u);
                 tmem_ld_wait();
-                float v[8];
+                float v[kCols];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(u[k]);
+                for (int k = 0; k < kCols; ++k) v[k] = __uint_as_float(u[k]);
                 if (mine) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) __stcg(mine + (c + k) * kGM, v[k]);
+                    for (int k = 0; k < kCols; ++k)
+                        if (c + (k & ~7) < p.r) __stcg(mine + (c + k) * kGM, v[k]);
                 } else {
                     store(c, v);
                 }
@@ -401,14 +416,25 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
                 const bool last = *reinterpret_cast<volatile int*>(&ctl->last) != 0;
                 if (last) {
                     __threadfence();
-                    for (int c = 0; c < p.r; c += 8) {
-                        float v[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] = 0.f;
-                        for (int64_t j = c_lo; j <= c_hi; ++j) {
+                    // in block order; a part's columns are all in flight together, and the
+                    // next part's with them
+                    for (int c = 0; c < p.r; c += kCols) {
+                        auto load = [&](int64_t j, float (&x)[kCols]) {
                             const float* part = p.sums + (2 * j + (j == c_lo ? 1 : 0)) * slot + row;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) v[k] += __ldcg(part + (c + k) * kGM);
+                            for (int k = 0; k < kCols; ++k) x[k] = c + (k & ~7) < p.r ? __ldcg(part + (c + k) * kGM) : 0.f;
+                        };
+                        float v[kCols], x[kCols];
+                        load(c_lo, v);
+                        load(c_lo + 1, x);  // (at least two parts)
+                        for (int64_t j = c_lo + 1; j <= c_hi; ++j) {
+                            float y[kCols];
+                            if (j < c_hi) load(j + 1, y);
+#pragma unroll
+                            for (int k = 0; k < kCols; ++k) {
+                                v[k] += x[k];
+                                x[k] = y[k];
+                            }
                         }
                         store(c, v);
                     }
