@@ -137,8 +137,22 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
     // the CTAs that share the list: none without a block, else kGMinBlocks each
     const int64_t fit = total / kGMinBlocks > 1 ? total / kGMinBlocks : 1;
     const int64_t G = fit < gridDim.x ? fit : gridDim.x;
+    // Share j ends where share j + 1 begins, at total (j + 1) / G or at an end of the item
+    // there if that is near: an eighth of a share more work costs less than joining parts.
+    const int64_t near = total / G / 8 > 1 ? total / G / 8 : 1;
+    auto snap = [&](int64_t x, int64_t begin, int64_t end) {  // x in the item [begin, end)
+        if (x - begin <= near && x - begin <= end - x) return begin;
+        return end - x <= near ? end : x;
+    };
+    auto bound = [&](int64_t j) {
+        const int64_t x = total * j / G;
+        if (x >= total) return total;
+        const int64_t tile = x / nblocks, base = tile * nblocks;
+        const int a = p.plan.block[x - base].x;
+        return snap(x, base + p.plan.boff[a], base + p.plan.boff[a + 1]);
+    };
     const bool idle = blockIdx.x >= G;
-    const int64_t lo = idle ? 0 : total * blockIdx.x / G, hi = idle ? 0 : total * (blockIdx.x + 1) / G;
+    const int64_t lo = idle ? 0 : bound(blockIdx.x), hi = idle ? 0 : bound(blockIdx.x + 1);
 
     // The list runs chunk by chunk through all adapters' blocks, so that blocks that have
     // to be gathered (3x a copied one's time) fall to all CTAs alike.
@@ -350,8 +364,11 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
             const int64_t i_lo = w.at - w.b, i_hi = i_lo + w.nb;
             int64_t c_lo = blockIdx.x, c_hi = blockIdx.x;
             if (i_lo < lo || i_hi > hi) {
+                // (the shares at its ends, but for those whose bounds went to its ends)
                 c_lo = ((i_lo + 1) * G - 1) / total;
                 c_hi = (i_hi * G - 1) / total;
+                for (int64_t x; (x = total * (c_lo + 1) / G) < i_hi && snap(x, i_lo, i_hi) == i_lo;) ++c_lo;
+                for (int64_t x; (x = total * c_hi / G) > i_lo && snap(x, i_lo, i_hi) == i_hi;) --c_hi;
             }
             next_item(w);  // (its loads before the wait)
             const int sd = tile < p.side[0].tiles ? 0 : 1;
