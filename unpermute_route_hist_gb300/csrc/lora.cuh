@@ -121,26 +121,68 @@ __device__ __forceinline__ uint32_t idesc_bf16_f32_n(int M, int N, int a_mn_majo
     return (idesc_bf16_f32(M, 0, a_mn_major, b_mn_major)) | (static_cast<uint32_t>(N >> 3) << 17);
 }
 
-// D[tmem] += A[smem] * B[smem]^T for the rows whose mask bit is set; the other
-// rows' accumulators are not written (the MMA's disable-output-lane operand).
-__device__ __forceinline__ void umma_bf16_rows(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                               const uint32_t (&keep)[4]) {
+// The producer and issuer warps run as whole warps: every lane walks the loop and
+// waits, one elected lane issues.  Addresses and descriptors then are the same in every
+// lane, which lets them live in uniform registers; with lane 0 alone on a divergent
+// path the issuer needed 562 cycles for a block of four MMAs whatever their width,
+// 505 (256 columns) and 375 (64 columns) this way.
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0); }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// Every lane waits for the phase; true if all of them saw it (bounded, as mbar_wait).
+__device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status,
+                                         bool cluster_scope = false) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, 0, kWaitLimitNs, cluster_scope));
+}
+
+// A descriptor as its two halves: addresses advance the low one (16-byte units).
+struct Desc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ explicit Desc(uint64_t d) : lo(static_cast<uint32_t>(d)), hi(static_cast<uint32_t>(d >> 32)) {}
+};
+
+// D[tmem] (+)= A[smem] * B[smem]^T, a and b units of 16 bytes past the descriptors.
+template <bool PAIR>
+__device__ __forceinline__ void umma_at(uint32_t d_tmem, const Desc& A, uint32_t a, const Desc& B, uint32_t b,
+                                        uint32_t idesc, uint32_t accumulate) {
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+            "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+            "r"(A.lo + a), "r"(A.hi), "r"(B.lo + b), "r"(B.hi), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+            "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+            "r"(A.lo + a), "r"(A.hi), "r"(B.lo + b), "r"(B.hi), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+// D[tmem] += A[smem] * B[smem]^T for the rows whose mask bit is set; the other rows'
+// accumulators are not written (the MMA's disable-output-lane operand).
+__device__ __forceinline__ void umma_rows_at(uint32_t d_tmem, const Desc& A, uint32_t a, const Desc& B, uint32_t b,
+                                             uint32_t idesc, const uint32_t (&keep)[4]) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, 1, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(~keep[0]), "r"(~keep[1]), "r"(~keep[2]), "r"(~keep[3])
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.ne.b32 p, 1, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, {%6, %7, %8, %9}, p;\n\t}" ::"r"(d_tmem),
+        "r"(A.lo + a), "r"(A.hi), "r"(B.lo + b), "r"(B.hi), "r"(idesc), "r"(~keep[0]), "r"(~keep[1]), "r"(~keep[2]),
+        "r"(~keep[3])
         : "memory");
 }
-__device__ __forceinline__ void umma_bf16_rows_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                                    const uint32_t (&keep)[8]) {
+__device__ __forceinline__ void umma_rows_pair_at(uint32_t d_tmem, const Desc& A, uint32_t a, const Desc& B, uint32_t b,
+                                                  uint32_t idesc, const uint32_t (&keep)[8]) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, 1, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7, %8, %9, %10, %11}, p;\n\t}" ::"r"(
-            d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(~keep[0]), "r"(~keep[1]), "r"(~keep[2]), "r"(~keep[3]),
-        "r"(~keep[4]), "r"(~keep[5]), "r"(~keep[6]), "r"(~keep[7])
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.ne.b32 p, 1, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, {%6, %7, %8, %9, %10, %11, %12, %13}, p;\n\t}" ::"r"(d_tmem),
+        "r"(A.lo + a), "r"(A.hi), "r"(B.lo + b), "r"(B.hi), "r"(idesc), "r"(~keep[0]), "r"(~keep[1]), "r"(~keep[2]),
+        "r"(~keep[3]), "r"(~keep[4]), "r"(~keep[5]), "r"(~keep[6]), "r"(~keep[7])
         : "memory");
 }
 

@@ -29,7 +29,7 @@ constexpr int kGK = kBlockRows;     // rows of a block
 constexpr int kGThreads = 320;      // producer, issuer, four gather and four epilogue warps
 constexpr int kGWide = kGM * kGK * 2;
 constexpr int kGMaxStages = 8;
-constexpr int kGMinBlocks = 4;      // of a CTA's share
+constexpr int kGMinBlocks = 2;      // of a CTA's share
 
 struct GradSide {
     const uint16_t* wide;      // [T, cols]
@@ -102,11 +102,34 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
     __shared__ GradCtl ctl_s;
     GradCtl* ctl = &ctl_s;
     volatile int* abort_flag = &ctl->abort_flag;
-    const int warp = warp_id(), lane = lane_id();
+    const int warp = warp_index(), lane = lane_id();
     const int tiles = p.side[0].tiles + p.side[1].tiles;
     const int ncols = CHUNK * p.nc;  // accumulator columns
     const int buf_cols = ncols <= 16 ? 16 : (ncols <= 32 ? 32 : (ncols <= 64 ? 64 : (ncols <= 128 ? 128 : 256)));
     constexpr uint32_t piece_bytes = CHUNK * kGK * 2;
+
+    // adapters without tokens get zeros, a piece from every CTA: a lane looks at an
+    // adapter, the warp clears those found
+    for (int a0 = warp * 32; a0 < p.plan.L; a0 += kGThreads) {
+        const int mine = a0 + lane;
+        const bool empty = mine < p.plan.L && p.plan.boff[mine + 1] == p.plan.boff[mine];
+        for (uint32_t found = __ballot_sync(0xffffffffu, empty); found; found &= found - 1) {
+            const int a = a0 + __ffs(found) - 1;
+            for (int k = 0; k < 2; ++k) {
+                if (!p.side[k].tiles) continue;
+                const int64_t n = static_cast<int64_t>(p.r) * p.side[k].cols;
+                for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * 8; i < n;
+                     i += static_cast<int64_t>(gridDim.x) * 256)
+                    *reinterpret_cast<uint4*>(p.side[k].out + a * n + i) = make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
+    const int nblocks = p.plan.boff[p.plan.L];
+    const int64_t total = static_cast<int64_t>(nblocks) * tiles;
+    // the CTAs that share the list: none without a block, else kGMinBlocks each
+    const int64_t fit = total / kGMinBlocks > 1 ? total / kGMinBlocks : 1;
+    const int64_t G = fit < gridDim.x ? fit : gridDim.x;
+    if (blockIdx.x >= G) return;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -132,11 +155,6 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
     const uint32_t ring0 = smem_u32(ring);
-    const int nblocks = p.plan.boff[p.plan.L];
-    const int64_t total = static_cast<int64_t>(nblocks) * tiles;
-    // the CTAs that share the list: none without a block, else kGMinBlocks each
-    const int64_t fit = total / kGMinBlocks > 1 ? total / kGMinBlocks : 1;
-    const int64_t G = fit < gridDim.x ? fit : gridDim.x;
     // Share j ends where share j + 1 begins, at total (j + 1) / G or at an end of the item
     // there if that is near: an eighth of a share more work costs less than joining parts.
     const int64_t near = total / G / 8 > 1 ? total / G / 8 : 1;
@@ -146,13 +164,12 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
     };
     auto bound = [&](int64_t j) {
         const int64_t x = total * j / G;
-        if (x >= total) return total;
+        if (x >= total) return total;  // (and with no blocks at all)
         const int64_t tile = x / nblocks, base = tile * nblocks;
         const int a = p.plan.block[x - base].x;
         return snap(x, base + p.plan.boff[a], base + p.plan.boff[a + 1]);
     };
-    const bool idle = blockIdx.x >= G;
-    const int64_t lo = idle ? 0 : bound(blockIdx.x), hi = idle ? 0 : bound(blockIdx.x + 1);
+    const int64_t lo = bound(blockIdx.x), hi = bound(blockIdx.x + 1);
 
     // The list runs chunk by chunk through all adapters' blocks, so that blocks that have
     // to be gathered (3x a copied one's time) fall to all CTAs alike.
@@ -184,24 +201,25 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
 
     if (warp == 0) {
         // --------------------------------------------------- TMA producer --
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            int64_t issued = 0;
-            int tile = lo < hi ? static_cast<int>(lo / nblocks) : 0;
-            int in = static_cast<int>(lo - static_cast<int64_t>(tile) * nblocks);
-            int4 next = lo < hi ? p.plan.block[in] : make_int4(0, 0, 0, 0);
-            for (int64_t at = lo; at < hi; ++at) {
-                const int4 e = next;
-                const int t = tile;
-                if (++in == nblocks) { in = 0; ++tile; }
-                next = p.plan.block[in];  // on its way while this one waits
-                const int sd = t < p.side[0].tiles ? 0 : 1;
-                const int col0 = (sd == 0 ? t : t - p.side[0].tiles) * kGM;
-                const int parts = sd == 0 ? p.side[0].parts : p.side[1].parts;
-                if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) break;
-                uint64_t* bar = &ctl->full[stage];
-                const bool tma = by_tma(e);
+        const bool elect = elect_one();
+        int stage = 0;
+        uint32_t phase = 0;
+        int64_t issued = 0;
+        int tile = lo < hi ? static_cast<int>(lo / nblocks) : 0;
+        int in = static_cast<int>(lo - static_cast<int64_t>(tile) * nblocks);
+        int4 next = lo < hi ? p.plan.block[in] : make_int4(0, 0, 0, 0);
+        for (int64_t at = lo; at < hi; ++at) {
+            const int4 e = next;
+            const int t = tile;
+            if (++in == nblocks) { in = 0; ++tile; }
+            next = p.plan.block[in];  // on its way while this one waits
+            const int sd = t < p.side[0].tiles ? 0 : 1;
+            const int col0 = (sd == 0 ? t : t - p.side[0].tiles) * kGM;
+            const int parts = sd == 0 ? p.side[0].parts : p.side[1].parts;
+            if (!all_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) break;
+            uint64_t* bar = &ctl->full[stage];
+            const bool tma = by_tma(e);
+            if (elect) {
                 ctl->kind[stage] = (tma ? 0 : kGathered) | ((e.z & kLastBlock) || at + 1 == hi ? kItemEnd : 0) |
                                    (parts == 2 ? kTwoParts : 0);
                 if (tma) {
@@ -216,62 +234,60 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
                 } else {
                     mbar_arrive(bar);
                 }
-                ++issued;
-                if (++stage == p.stages) { stage = 0; phase ^= 1u; }
             }
-            // every copy has landed before the CTA exits
-            const int64_t pend = issued < p.stages ? issued : p.stages;
-            for (int64_t j = 0; j < pend; ++j) {
-                if (--stage < 0) { stage = p.stages - 1; phase ^= 1u; }
-                int dummy = 0;
-                mbar_wait(&ctl->full[stage], phase, reinterpret_cast<volatile int*>(&dummy), p.status);
-            }
+            ++issued;
+            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+        }
+        // every copy has landed before the CTA exits
+        const int64_t pend = issued < p.stages ? issued : p.stages;
+        for (int64_t j = 0; j < pend; ++j) {
+            if (--stage < 0) { stage = p.stages - 1; phase ^= 1u; }
+            int dummy = 0;
+            mbar_wait(&ctl->full[stage], phase, reinterpret_cast<volatile int*>(&dummy), p.status);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ----------------------------------------------------- MMA issuer --
-        if (lane == 0) {
-            const uint32_t idesc = idesc_bf16_f32_n(kGM, ncols, 1, 1);
-            // descriptors of stage 0; an address advances by its bytes / 16
-            const uint64_t wide0 = smem_desc(ring0, kGWide / 2, 1024, kLayoutSw128);
-            const uint64_t narrow0 = mnmajor_desc(ring0 + kGWide, 2 * CHUNK, piece_bytes);
-            constexpr uint32_t narrow_step = 2 * CHUNK;
-            const uint32_t part_step = p.nc * piece_bytes / 16;
-            int stage = 0;
-            uint32_t phase = 0, item = 0;
-            bool any_mma = false, first = true;
-            for (int64_t at = lo; at < hi; ++at) {
-                const uint32_t buf = item & 1u;
-                if (first && !mbar_wait(&ctl->acc_empty[buf], ((item >> 1) & 1u) ^ 1u, abort_flag, p.status)) break;
-                if (!mbar_wait(&ctl->full[stage], phase, abort_flag, p.status)) break;
-                tc_fence_after();
-                const int kind = *reinterpret_cast<volatile int*>(&ctl->kind[stage]);
+        const bool elect = elect_one();
+        const uint32_t idesc = idesc_bf16_f32_n(kGM, ncols, 1, 1);
+        const Desc dWide(smem_desc(ring0, kGWide / 2, 1024, kLayoutSw128));
+        const Desc dNarrow(mnmajor_desc(ring0 + kGWide, 2 * CHUNK, piece_bytes));
+        constexpr uint32_t kStep = 2 * CHUNK;  // 16 rows of the narrow operand (the wide one's: 128)
+        const uint32_t part_step = p.nc * piece_bytes / 16;
+        int stage = 0;
+        uint32_t phase = 0, item = 0;
+        bool any_mma = false, first = true;
+        for (int64_t at = lo; at < hi; ++at) {
+            const uint32_t buf = item & 1u;
+            if (first && !all_wait(&ctl->acc_empty[buf], ((item >> 1) & 1u) ^ 1u, abort_flag, p.status)) break;
+            if (!all_wait(&ctl->full[stage], phase, abort_flag, p.status)) break;
+            tc_fence_after();
+            const int kind = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&ctl->kind[stage]), 0);
+            const uint32_t off = stage * (p.stage_bytes / 16);
+            const uint32_t d = tmem + buf * buf_cols;
+            const bool end = (kind & kItemEnd) != 0;
+            if (elect) {
                 if (kind & kGathered) fence_proxy_async_smem();  // gathered rows are generic-proxy writes
-                const uint32_t off = stage * p.stage_bytes / 16;
-                const uint32_t d = tmem + buf * buf_cols;
 #pragma unroll
                 for (int ks = 0; ks < kGK / 16; ++ks)
-                    umma_bf16(d, wide0 + off + ks * 128, narrow0 + off + ks * narrow_step, idesc,
-                              (!first || ks > 0) ? 1u : 0u);
+                    umma_at<false>(d, dWide, off + ks * 128, dNarrow, off + ks * kStep, idesc, (!first || ks > 0) ? 1u : 0u);
                 if (kind & kTwoParts) {
 #pragma unroll
                     for (int ks = 0; ks < kGK / 16; ++ks)
-                        umma_bf16(d, wide0 + off + ks * 128, narrow0 + off + part_step + ks * narrow_step, idesc, 1u);
+                        umma_at<false>(d, dWide, off + ks * 128, dNarrow, off + part_step + ks * kStep, idesc, 1u);
                 }
                 umma_commit(&ctl->empty[stage]);
-                any_mma = true;
-                if (++stage == p.stages) { stage = 0; phase ^= 1u; }
-                first = (kind & kItemEnd) != 0;
-                if (first) {
-                    umma_commit(&ctl->acc_full[buf]);
-                    ++item;
-                }
+                if (end) umma_commit(&ctl->acc_full[buf]);
             }
-            if (any_mma) {
-                umma_commit(&ctl->drain);
-                int dummy = 0;
-                mbar_wait(&ctl->drain, 0, reinterpret_cast<volatile int*>(&dummy), p.status);
-            }
+            any_mma = true;
+            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+            first = end;
+            if (end) ++item;
+        }
+        if (any_mma) {
+            if (elect) umma_commit(&ctl->drain);
+            int dummy = 0;
+            mbar_wait(&ctl->drain, 0, reinterpret_cast<volatile int*>(&dummy), p.status);
         }
         __syncwarp();
     } else if (warp < 6) {
@@ -462,16 +478,6 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
         }
     }
 
-    // adapters without tokens get zeros
-    for (int a = blockIdx.x; a < p.plan.L; a += gridDim.x) {
-        if (p.plan.boff[a + 1] != p.plan.boff[a]) continue;
-        for (int k = 0; k < 2; ++k) {
-            if (!p.side[k].tiles) continue;
-            const int64_t n = static_cast<int64_t>(p.r) * p.side[k].cols;
-            for (int64_t i = threadIdx.x * 8; i < n; i += kGThreads * 8)
-                *reinterpret_cast<uint4*>(p.side[k].out + a * n + i) = make_uint4(0, 0, 0, 0);
-        }
-    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -496,12 +502,8 @@ int launch_grad(const GradMaps& m, GradParams p, cudaStream_t st) {
     }
     p.stages = RING / p.stage_bytes;
     if (p.stages > kGMaxStages) p.stages = kGMaxStages;
-    // every CTA resident at once, none with less than kGMinBlocks blocks of the
-    // blocks there can be
-    int64_t G = p.plan.max_blocks * (p.side[0].tiles + p.side[1].tiles) / kGMinBlocks;
-    if (G > int64_t(CTAS) * num_sms()) G = int64_t(CTAS) * num_sms();
+    int64_t G = int64_t(CTAS) * num_sms();  // every CTA resident at once
     if (G > kGradCtas) G = kGradCtas;
-    if (G < 1) G = 1;
     clear_pending_launch_error();
     grad_kernel<RING, CTAS, CHUNK><<<static_cast<unsigned>(G), kGThreads, smem, st>>>(m, p);
     return launch_result();

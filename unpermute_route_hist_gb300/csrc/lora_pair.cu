@@ -71,7 +71,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                                                ~static_cast<uintptr_t>(1023));
     PairCtl* ctl = reinterpret_cast<PairCtl*>(ring + kPStages * kPStage);
     volatile int* abort_flag = &ctl->abort_flag;
-    const int warp = warp_id(), lane = lane_id();
+    const int warp = warp_index(), lane = lane_id();
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int64_t slot = cluster_id_x(), nslot = nclusters_x();
@@ -110,7 +110,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
 
     if (warp == 0) {
         // ------------------------------------------------------- producer --
-        if (lane == 0) {
+        {
+            const bool elect = elect_one();
             int stage = 0;
             uint32_t phase = 0;
             int64_t issued = 0;
@@ -123,18 +124,20 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                 const int ne = p.plan.cnt[ti.unit];
                 const int32_t* gid = p.plan.gid + ti.unit * p.plan.slots;
                 for (int i = 0; i < nb; ++i) {
-                    if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+                    if (!all_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
                     uint8_t* sA = ring + stage * kPStage;
                     uint8_t* sB = sA + kPSlot;
                     const uint32_t bar = mapa_u32(&ctl->full[stage], 0);
                     const int32_t red = i * kPK;
-                    if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2 * kPStage);
-                    tma_load_2d_pair(sA, &tmX, bar, red, arow);
-                    if (B_MN) {
-                        tma_load_2d_pair(sB, &tmW, bar, nh, red);
-                        tma_load_2d_pair(sB + 8192, &tmW, bar, nh + 64, red);
-                    } else {
-                        tma_load_2d_pair(sB, &tmW, bar, red, nh);
+                    if (elect) {
+                        if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2 * kPStage);
+                        tma_load_2d_pair(sA, &tmX, bar, red, arow);
+                        if (B_MN) {
+                            tma_load_2d_pair(sB, &tmW, bar, nh, red);
+                            tma_load_2d_pair(sB + 8192, &tmW, bar, nh + 64, red);
+                        } else {
+                            tma_load_2d_pair(sB, &tmW, bar, red, nh);
+                        }
                     }
                     ++issued;
                     if (++stage == kPStages) { stage = 0; phase ^= 1u; }
@@ -154,21 +157,23 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                     const int rc = p.r <= 64 ? 0 : (xi % rchunks) * 64;
                     const int32_t now[4] = {g[0], g[1], g[2], g[3]};
                     if (xi + 1 < xb) load_ids(xi + 1);
-                    if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+                    if (!all_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
                     if (!waited) { pdl_wait(); waited = true; }  // U (V) of the kernel before
                     uint8_t* sA = ring + stage * kPStage;
                     uint8_t* sB = sA + kPSlot;
                     const uint32_t bar = mapa_u32(&ctl->full[stage], 0);
-                    if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2u * (eb + eb * en));
-                    tma_load_2d_pair(sA, &tmU, bar, rc, arow);
+                    if (elect) {
+                        if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2u * (eb + eb * en));
+                        tma_load_2d_pair(sA, &tmU, bar, rc, arow);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (e >= en) break;
-                        if (B_MN) {
-                            tma_load_3d_pair(sB + e * eb, &tmE, bar, nh, rc, now[e]);
-                            tma_load_3d_pair(sB + e * eb + eb / 2, &tmE, bar, nh + 64, rc, now[e]);
-                        } else {
-                            tma_load_3d_pair(sB + e * eb, &tmE, bar, rc, nh, now[e]);
+                        for (int e = 0; e < 4; ++e) {
+                            if (e >= en) break;
+                            if (B_MN) {
+                                tma_load_3d_pair(sB + e * eb, &tmE, bar, nh, rc, now[e]);
+                                tma_load_3d_pair(sB + e * eb + eb / 2, &tmE, bar, nh + 64, rc, now[e]);
+                            } else {
+                                tma_load_3d_pair(sB + e * eb, &tmE, bar, rc, nh, now[e]);
+                            }
                         }
                     }
                     ++issued;
@@ -188,8 +193,17 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
         }
     } else if (warp == 1) {
         // ----------------------------------------------------- MMA issuer --
-        if (leader && lane == 0) {
+        if (leader) {
+            const bool elect = elect_one();
             constexpr uint32_t idesc = idesc_bf16_f32(2 * kPM, kPN, 0, B_MN ? 1 : 0);
+            // stage 0's operands: the shared product's, the adapters'
+            const uint32_t eb = 256u * p.rpad;
+            const Desc dX(smem_desc(ring0, 16, 1024, kLayoutSw128));
+            const Desc dW(B_MN ? smem_desc(ring0 + kPSlot, 8192, 1024, kLayoutSw128)
+                               : smem_desc(ring0 + kPSlot, 16, 1024, kLayoutSw128));
+            const Desc dU(kmajor_desc(ring0, p.rpad * 2));
+            const Desc dE(B_MN ? smem_desc(ring0 + kPSlot, eb / 2, 1024, kLayoutSw128) : kmajor_desc(ring0 + kPSlot, p.rpad * 2));
+            constexpr uint32_t kStep = B_MN ? 128 : 2;  // 16 reduction columns of the right operand
             int stage = 0;
             uint32_t phase = 0, acc = 0;
             bool ok = true, any_mma = false;
@@ -197,8 +211,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                 const PairTile ti = pair_tile(t, p);
                 const int ne = p.plan.cnt[ti.unit];
                 const uint4* masks = reinterpret_cast<const uint4*>(p.plan.mask + ti.unit * p.plan.slots * kUnitWords);
-                // the rows of a block's adapters, loaded one block ahead (the first tile's
-                // with its shared blocks still to come)
+                // the rows of a block's adapters, loaded one block ahead (the first block's
+                // with the shared product's still to come)
                 uint4 m[4][2];
                 auto load_masks = [&](int xi) {
                     const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
@@ -211,23 +225,19 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                 };
                 load_masks(0);
                 const uint32_t buf = acc & 1u;
-                if (!mbar_wait(&ctl->tmem_empty[buf], ((acc >> 1) & 1u) ^ 1u, abort_flag, p.status, 0, kWaitLimitNs,
-                               true))
-                    break;
+                if (!all_wait(&ctl->tmem_empty[buf], ((acc >> 1) & 1u) ^ 1u, abort_flag, p.status, true)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + buf * kPN;
                 for (int i = 0; i < nb; ++i) {
-                    if (!mbar_wait(&ctl->full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+                    if (!all_wait(&ctl->full[stage], phase, abort_flag, p.status)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t sA = ring0 + stage * kPStage, sB = sA + kPSlot;
+                    const uint32_t at = stage * (kPStage / 16);
+                    if (elect) {
 #pragma unroll
-                    for (int ks = 0; ks < kPK / 16; ++ks) {
-                        const uint64_t ad = smem_desc(sA + ks * 32, 16, 1024, kLayoutSw128);
-                        const uint64_t bd = B_MN ? smem_desc(sB + ks * 2048, 8192, 1024, kLayoutSw128)
-                                                 : smem_desc(sB + ks * 32, 16, 1024, kLayoutSw128);
-                        umma_bf16_pair(d, ad, bd, idesc, (i > 0 || ks > 0) ? 1u : 0u);
+                        for (int ks = 0; ks < kPK / 16; ++ks)
+                            umma_at<true>(d, dX, at + 2 * ks, dW, at + kStep * ks, idesc, (i > 0 || ks > 0) ? 1u : 0u);
+                        umma_commit_pair(&ctl->empty[stage], 0x3);
                     }
-                    umma_commit_pair(&ctl->empty[stage], 0x3);
                     any_mma = true;
                     if (++stage == kPStages) { stage = 0; phase ^= 1u; }
                 }
@@ -235,30 +245,30 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                 for (int xi = 0; xi < xb && ok; ++xi) {
                     const int en = p.r <= 64 ? min(p.epb, ne - xi * p.epb) : 1;
                     const int left = p.r <= 64 ? p.r : min(64, p.r - (xi % rchunks) * 64);
-                    if (!mbar_wait(&ctl->full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+                    const int steps = (left + 15) / 16;
+                    if (!all_wait(&ctl->full[stage], phase, abort_flag, p.status)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t sA = ring0 + stage * kPStage, sB = sA + kPSlot;
-                    const uint32_t eb = 256u * p.rpad;
+                    const uint32_t at = stage * (kPStage / 16);
+                    if (elect) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (e >= en) break;
-                        const uint32_t keep[8] = {m[e][0].x, m[e][0].y, m[e][0].z, m[e][0].w,
-                                                  m[e][1].x, m[e][1].y, m[e][1].z, m[e][1].w};
-                        for (int ks = 0; ks < (left + 15) / 16; ++ks) {
-                            const uint64_t ad = kmajor_desc(sA + ks * 32, p.rpad * 2);
-                            const uint64_t bd = B_MN ? smem_desc(sB + e * eb + ks * 2048, eb / 2, 1024, kLayoutSw128)
-                                                     : kmajor_desc(sB + e * eb + ks * 32, p.rpad * 2);
-                            umma_bf16_rows_pair(d, ad, bd, idesc, keep);
+                        for (int e = 0; e < 4; ++e) {
+                            if (e >= en) break;
+                            const uint32_t keep[8] = {m[e][0].x, m[e][0].y, m[e][0].z, m[e][0].w,
+                                                      m[e][1].x, m[e][1].y, m[e][1].z, m[e][1].w};
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                if (ks < steps)
+                                    umma_rows_pair_at(d, dU, at + 2 * ks, dE, at + e * (eb / 16) + kStep * ks, idesc, keep);
                         }
+                        umma_commit_pair(&ctl->empty[stage], 0x3);
                     }
-                    umma_commit_pair(&ctl->empty[stage], 0x3);
                     if (xi + 1 < xb) load_masks(xi + 1);
                     if (++stage == kPStages) { stage = 0; phase ^= 1u; }
                 }
-                if (ok) umma_commit_pair(&ctl->tmem_full[buf], 0x3);
+                if (ok && elect) umma_commit_pair(&ctl->tmem_full[buf], 0x3);
             }
             if (any_mma) {
-                umma_commit_pair(&ctl->drain, 0x1);
+                if (elect) umma_commit_pair(&ctl->drain, 0x1);
                 int dummy = 0;
                 mbar_wait(&ctl->drain, 0, reinterpret_cast<volatile int*>(&dummy), p.status);
             }

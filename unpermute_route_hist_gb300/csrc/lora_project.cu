@@ -64,7 +64,7 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                                                ~static_cast<uintptr_t>(1023));
     ProjectCtl* ctl = reinterpret_cast<ProjectCtl*>(ring + kRRing);
     volatile int* abort_flag = &ctl->abort_flag;
-    const int warp = warp_id(), lane = lane_id();
+    const int warp = warp_index(), lane = lane_id();
     const int rank = static_cast<int>(cluster_ctarank());
     const int64_t item = blockIdx.x / S;
     // a column tile's row tiles are neighbours: they read the same W
@@ -152,24 +152,25 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
 
     if (warp == 0) {
         // ------------------------------------------------------- producer --
-        if (lane == 0) {
-            int issued = min(nbase, stages);
-            int stage = issued % stages;
-            uint32_t phase = issued == stages ? 1u : 0u;
-            bool waited = false;
-            for (int i = issued; i < nblk; ++i) {
-                if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) break;
-                if (i < nbase) {
-                    load_base(i, stage);
-                } else {
-                    if (!waited) { pdl_wait(); waited = true; }  // U (V) of the kernel before
-                    uint8_t* sA = ring + stage * stage_bytes;
-                    uint8_t* sB = sA + a_slot;
-                    uint64_t* bar = &ctl->full[stage];
-                    const int xi = x_lo + i - nbase;
-                    const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
-                    const int en = p.r <= 64 ? min(p.epb, ne - ef) : 1;
-                    const int rc = p.r <= 64 ? 0 : (xi % rchunks) * 64;
+        const bool elect = elect_one();
+        int issued = min(nbase, stages);
+        int stage = issued % stages;
+        uint32_t phase = issued == stages ? 1u : 0u;
+        bool waited = false;
+        for (int i = issued; i < nblk; ++i) {
+            if (!all_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) break;
+            if (i < nbase) {
+                if (elect) load_base(i, stage);
+            } else {
+                if (!waited) { pdl_wait(); waited = true; }  // U (V) of the kernel before
+                uint8_t* sA = ring + stage * stage_bytes;
+                uint8_t* sB = sA + a_slot;
+                uint64_t* bar = &ctl->full[stage];
+                const int xi = x_lo + i - nbase;
+                const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
+                const int en = p.r <= 64 ? min(p.epb, ne - ef) : 1;
+                const int rc = p.r <= 64 ? 0 : (xi % rchunks) * 64;
+                if (elect) {
                     mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.xrows) * p.rpad * 2u + eb * en);
                     tma_load_2d(sA, &tmU, bar, rc, static_cast<int32_t>(row0));
                     for (int e = 0; e < en; ++e) {
@@ -182,57 +183,63 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                         }
                     }
                 }
-                ++issued;
-                if (++stage == stages) { stage = 0; phase ^= 1u; }
             }
-            if (!waited) pdl_wait();  // the launch before this one has finished before this grid can
-            // every copy has landed before the ring is reused or the CTA exits
-            for (int j = 0; j < min(issued, stages); ++j) {
-                if (--stage < 0) { stage = stages - 1; phase ^= 1u; }
-                int dummy = 0;
-                mbar_wait(&ctl->full[stage], phase, reinterpret_cast<volatile int*>(&dummy), p.status);
-            }
+            ++issued;
+            if (++stage == stages) { stage = 0; phase ^= 1u; }
+        }
+        if (!waited) pdl_wait();  // the launch before this one has finished before this grid can
+        // every copy has landed before the ring is reused or the CTA exits
+        for (int j = 0; j < min(issued, stages); ++j) {
+            if (--stage < 0) { stage = stages - 1; phase ^= 1u; }
+            int dummy = 0;
+            mbar_wait(&ctl->full[stage], phase, reinterpret_cast<volatile int*>(&dummy), p.status);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ----------------------------------------------------- MMA issuer --
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            bool any_mma = false;
-            constexpr uint32_t idesc = idesc_bf16_f32(kRM, kRN, 0, B_MN ? 1 : 0);
-            for (int i = 0; i < nblk; ++i) {
-                if (!mbar_wait(&ctl->full[stage], phase, abort_flag, p.status)) break;
-                tc_fence_after();
-                const uint32_t sA = ring0 + stage * stage_bytes, sB = sA + a_slot;
-                if (i < nbase) {
+        const bool elect = elect_one();
+        int stage = 0;
+        uint32_t phase = 0;
+        bool any_mma = false;
+        constexpr uint32_t idesc = idesc_bf16_f32(kRM, kRN, 0, B_MN ? 1 : 0);
+        const Desc dX(smem_desc(ring0, 16, 1024, kLayoutSw128));
+        const Desc dW(B_MN ? smem_desc(ring0 + a_slot, kRSlot / 2, 1024, kLayoutSw128)
+                           : smem_desc(ring0 + a_slot, 16, 1024, kLayoutSw128));
+        const Desc dU(kmajor_desc(ring0, p.rpad * 2));
+        const Desc dE(B_MN ? smem_desc(ring0 + a_slot, eb / 2, 1024, kLayoutSw128) : kmajor_desc(ring0 + a_slot, p.rpad * 2));
+        constexpr uint32_t kStep = B_MN ? 128 : 2;  // 16 reduction columns of the right operand
+        for (int i = 0; i < nblk; ++i) {
+            if (!all_wait(&ctl->full[stage], phase, abort_flag, p.status)) break;
+            tc_fence_after();
+            const uint32_t at = stage * (stage_bytes / 16);
+            if (i < nbase) {
+                if (elect) {
 #pragma unroll
-                    for (int ks = 0; ks < kRK / 16; ++ks) {
-                        const uint64_t ad = smem_desc(sA + ks * 32, 16, 1024, kLayoutSw128);
-                        const uint64_t bd = B_MN ? smem_desc(sB + ks * 2048, kRSlot / 2, 1024, kLayoutSw128)
-                                                 : smem_desc(sB + ks * 32, 16, 1024, kLayoutSw128);
-                        umma_bf16(tmem, ad, bd, idesc, (i > 0 || ks > 0) ? 1u : 0u);
-                    }
-                } else {
-                    const int xi = x_lo + i - nbase;
-                    const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
-                    const int en = p.r <= 64 ? min(p.epb, ne - ef) : 1;
-                    const int left = p.r <= 64 ? p.r : min(64, p.r - (xi % rchunks) * 64);
-                    for (int e = 0; e < en; ++e) {
-                        const uint32_t keep[4] = {ctl->mask[ef + e][0], ctl->mask[ef + e][1], ctl->mask[ef + e][2],
-                                                  ctl->mask[ef + e][3]};
-                        for (int ks = 0; ks < (left + 15) / 16; ++ks) {
-                            const uint64_t ad = kmajor_desc(sA + ks * 32, p.rpad * 2);
-                            const uint64_t bd = B_MN ? smem_desc(sB + e * eb + ks * 2048, eb / 2, 1024, kLayoutSw128)
-                                                     : kmajor_desc(sB + e * eb + ks * 32, p.rpad * 2);
-                            umma_bf16_rows(tmem, ad, bd, idesc, keep);
-                        }
+                    for (int ks = 0; ks < kRK / 16; ++ks)
+                        umma_at<false>(tmem, dX, at + 2 * ks, dW, at + kStep * ks, idesc, (i > 0 || ks > 0) ? 1u : 0u);
+                }
+            } else {
+                const int xi = x_lo + i - nbase;
+                const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
+                const int en = p.r <= 64 ? min(p.epb, ne - ef) : 1;
+                const int left = p.r <= 64 ? p.r : min(64, p.r - (xi % rchunks) * 64);
+                const int steps = (left + 15) / 16;
+                for (int e = 0; e < en; ++e) {
+                    const uint32_t keep[4] = {ctl->mask[ef + e][0], ctl->mask[ef + e][1], ctl->mask[ef + e][2],
+                                              ctl->mask[ef + e][3]};
+                    if (elect) {
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            if (ks < steps)
+                                umma_rows_at(tmem, dU, at + 2 * ks, dE, at + e * (eb / 16) + kStep * ks, idesc, keep);
                     }
                 }
-                umma_commit(&ctl->empty[stage]);
-                any_mma = true;
-                if (++stage == stages) { stage = 0; phase ^= 1u; }
             }
+            if (elect) umma_commit(&ctl->empty[stage]);
+            any_mma = true;
+            if (++stage == stages) { stage = 0; phase ^= 1u; }
+        }
+        if (elect) {
             if (any_mma) umma_commit(&ctl->done);
             else mbar_arrive(&ctl->done);
         }

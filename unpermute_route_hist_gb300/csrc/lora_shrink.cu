@@ -60,7 +60,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
                                                ~static_cast<uintptr_t>(1023));
     ShrinkCtl* ctl = reinterpret_cast<ShrinkCtl*>(ring + kSRing);
     volatile int* abort_flag = &ctl->abort_flag;
-    const int warp = warp_id(), lane = lane_id();
+    const int warp = warp_index(), lane = lane_id();
     const int rank = static_cast<int>(cluster_ctarank());
     const int64_t item = blockIdx.x / S;
 
@@ -127,16 +127,17 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
 
     if (warp == 0) {
         // ------------------------------------------------------- producer --
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            int issued = 0;
-            const uint32_t ebytes = B_MN ? piece_bytes * pieces : static_cast<uint32_t>(p.take) * 128u;
-            for (int b = lo; b < hi; ++b) {
-                if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) break;
-                uint8_t* sA = ring + stage * p.stage_bytes;
-                uint8_t* sB = sA + p.a_slot;
-                uint64_t* bar = &ctl->full[stage];
+        const bool elect = elect_one();
+        int stage = 0;
+        uint32_t phase = 0;
+        int issued = 0;
+        const uint32_t ebytes = B_MN ? piece_bytes * pieces : static_cast<uint32_t>(p.take) * 128u;
+        for (int b = lo; b < hi; ++b) {
+            if (!all_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) break;
+            uint8_t* sA = ring + stage * p.stage_bytes;
+            uint8_t* sB = sA + p.a_slot;
+            uint64_t* bar = &ctl->full[stage];
+            if (elect) {
                 mbar_arrive_expect_tx(bar, ebytes + (gather ? 0u : static_cast<uint32_t>(p.a_slot)));
                 if (!gather) tma_load_2d(sA, &tmX, bar, b * kSK, tile.w);
                 if (B_MN) {
@@ -145,41 +146,44 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
                 } else {
                     tma_load_3d(sB, &tmE, bar, b * kSK, c0, a);
                 }
-                ++issued;
-                if (++stage == p.stages) { stage = 0; phase ^= 1u; }
             }
-            // every copy has landed before the ring is reused or the CTA exits
-            for (int j = 0; j < min(issued, p.stages); ++j) {
-                if (--stage < 0) { stage = p.stages - 1; phase ^= 1u; }
-                int dummy = 0;
-                mbar_wait(&ctl->full[stage], phase, reinterpret_cast<volatile int*>(&dummy), p.status);
-            }
+            ++issued;
+            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+        }
+        // every copy has landed before the ring is reused or the CTA exits
+        for (int j = 0; j < min(issued, p.stages); ++j) {
+            if (--stage < 0) { stage = p.stages - 1; phase ^= 1u; }
+            int dummy = 0;
+            mbar_wait(&ctl->full[stage], phase, reinterpret_cast<volatile int*>(&dummy), p.status);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ----------------------------------------------------- MMA issuer --
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            bool any_mma = false;
-            const int cols = B_MN ? pieces * p.chunk : (p.take + 15) / 16 * 16;
-            const uint32_t idesc = idesc_bf16_f32_n(kSM, cols, 0, B_MN ? 1 : 0);
-            for (int b = lo; b < hi; ++b) {
-                if (!mbar_wait(&ctl->full[stage], phase, abort_flag, p.status)) break;
-                tc_fence_after();
+        const bool elect = elect_one();
+        int stage = 0;
+        uint32_t phase = 0;
+        bool any_mma = false;
+        const int cols = B_MN ? pieces * p.chunk : (p.take + 15) / 16 * 16;
+        const uint32_t idesc = idesc_bf16_f32_n(kSM, cols, 0, B_MN ? 1 : 0);
+        const Desc dX(smem_desc(ring0, 16, 1024, kLayoutSw128));
+        const Desc dE(B_MN ? mnmajor_desc(ring0 + p.a_slot, 2 * p.chunk, piece_bytes)
+                           : smem_desc(ring0 + p.a_slot, 16, 1024, kLayoutSw128));
+        const uint32_t step = B_MN ? 2 * p.chunk : 2;  // 16 reduction columns of the adapter
+        for (int b = lo; b < hi; ++b) {
+            if (!all_wait(&ctl->full[stage], phase, abort_flag, p.status)) break;
+            tc_fence_after();
+            const uint32_t at = stage * (p.stage_bytes / 16);
+            if (elect) {
                 if (gather) fence_proxy_async_smem();  // gathered rows are generic-proxy writes
-                const uint32_t sA = ring0 + stage * p.stage_bytes, sB = sA + p.a_slot;
 #pragma unroll
-                for (int ks = 0; ks < kSK / 16; ++ks) {
-                    const uint64_t ad = smem_desc(sA + ks * 32, 16, 1024, kLayoutSw128);
-                    const uint64_t bd = B_MN ? mnmajor_desc(sB + ks * 32 * p.chunk, 2 * p.chunk, piece_bytes)
-                                             : smem_desc(sB + ks * 32, 16, 1024, kLayoutSw128);
-                    umma_bf16(tmem, ad, bd, idesc, (b > lo || ks > 0) ? 1u : 0u);
-                }
+                for (int ks = 0; ks < kSK / 16; ++ks)
+                    umma_at<false>(tmem, dX, at + 2 * ks, dE, at + step * ks, idesc, (b > lo || ks > 0) ? 1u : 0u);
                 umma_commit(&ctl->empty[stage]);
-                any_mma = true;
-                if (++stage == p.stages) { stage = 0; phase ^= 1u; }
             }
+            any_mma = true;
+            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+        }
+        if (elect) {
             if (any_mma) umma_commit(&ctl->done);
             else mbar_arrive(&ctl->done);
         }
