@@ -121,8 +121,8 @@ SHAPES = [
     # as many adapters as there may be, in one unit's plan and in several
     (256, 64, 72, 2048, 8, "mixed"), (600, 72, 64, 2048, 8, "mixed"),
     # long reductions of few tiles, split over clusters (forward: K, backward: N)
-    (300, 2640, 136, 3, 24, "mixed"), (300, 136, 2640, 3, 24, "mixed"), (513, 2640, 520, 5, 136, "runs"),
-    (513, 520, 2640, 5, 136, "runs"),
+    (300, 2904, 136, 3, 24, "mixed"), (300, 136, 2904, 3, 24, "mixed"), (513, 2904, 520, 5, 136, "runs"),
+    (513, 520, 2904, 5, 136, "runs"),
     # more pair tiles than a round of the GPU holds
     (2600, 264, 2056, 4, 24, "runs"), (2600, 136, 1800, 6, 72, "mixed"), (2600, 2056, 264, 4, 24, "runs"),
     (2600, 1800, 136, 6, 72, "mixed"), (2560, 200, 4856, 3, 8, "runs"), (2560, 4856, 200, 3, 8, "runs"),

@@ -23,15 +23,20 @@ int check_sizes(int64_t T, int L, int r, int64_t N, int64_t K) {
 size_t v_bytes(int64_t T, int r) { return (static_cast<size_t>(T) * r * 2 + 255) / 256 * 256; }
 constexpr size_t kCounterBytes = (kGradCtas * sizeof(uint32_t) + 255) / 256 * 256;
 
-// Y (or dX) from its operands.  Tiles with a split reduction where splitting pays: one
-// row tile (decode: 64 rows of 4096 x 4096 take 19 us split, 28 in 2-CTA tiles), or a
-// long reduction whose 2-CTA tiles leave half of the GPU idle (512 rows: 26 and 30 us).
-// 2-CTA tiles otherwise (512 rows of 2048 x 2048: 18 and 20 us; 1024 rows of 4096 x
-// 4096: 35 and 44).
+// Y (or dX) from its operands: tiles with a split reduction, or 2-CTA tiles.  Splitting
+// pays for few rows (64 of 4096 x 4096: 18 and 25 us; of 2048 x 2048: 14 both), and for
+// a long reduction, the adapters' blocks among it, whose 2-CTA tiles leave half of the
+// GPU idle (300 rows of 4096 x 4096, 4 adapters: 24 and 27; of 2048 x 2048, 16 mixed
+// adapters of rank 64: 19 and 24; 4 adapters: 19 and 16).
 int project(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, const uint16_t* ad,
             const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, int32_t* status, cudaStream_t st) {
-    const int64_t pairs = plan.units * ((ncols + 255) / 256), blocks = (Kred + 63) / 64;
-    if (plan.T <= 128 || (pairs * 4 < num_sms() && blocks > 40))
+    const int64_t pairs = plan.units * ((ncols + 255) / 256);
+    // reduction blocks of a tile, with those of the adapters that can occur in it
+    const int64_t rchunks = (r + 63) / 64, per = 64 / rank_pad(r);
+    const int64_t rows = plan.T < kUnit ? plan.T : kUnit;
+    const int64_t adapters = (plan.L < rows ? plan.L : rows) * rchunks / per;
+    const int64_t blocks = (Kred + 63) / 64 + adapters;
+    if (plan.T <= 64 || (pairs * 4 < num_sms() && blocks > 44))
         return lora_project_launch(b_mn, X, W, U, ad, plan, Kred, ncols, r, out, status, st);
     return lora_pair_launch(b_mn, X, W, U, ad, plan, Kred, ncols, r, out, status, st);
 }
