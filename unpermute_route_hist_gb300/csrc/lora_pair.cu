@@ -30,7 +30,9 @@ struct PairParams {
     PlanView plan;
     int Kred, ncols, r, rpad, epb;
     int ntiles;        // column tiles
-    int64_t tiles;     // all of them
+    int64_t whole;     // tiles done whole; the rest are cut into column pieces
+    int cuts;          // pieces of those: 1 or 2
+    int64_t items;     // tiles and pieces
     uint16_t* out;
     int st32;          // output rows start 32-byte aligned
     int32_t* status;
@@ -47,25 +49,33 @@ struct PairCtl {
 };
 constexpr int kPairSmem = 1024 + kPStages * kPStage + sizeof(PairCtl);
 
-// Tile t: groups of kPGroup units sweep every column tile, rows fastest, so the
-// tiles in flight share W's columns and X's rows in L2.
+// Item t: groups of kPGroup units sweep every column tile, rows fastest, so the tiles
+// in flight share W's columns and X's rows in L2.  The tiles of the last round, when
+// they are few, are cut into column pieces that more clusters share.
 struct PairTile {
     int64_t unit;
-    int n0;
+    int n0, width;
 };
 __device__ __forceinline__ PairTile pair_tile(int64_t t, const PairParams& p) {
+    int piece = 0, width = kPN;
+    if (t >= p.whole) {
+        width = kPN / p.cuts;
+        piece = static_cast<int>((t - p.whole) % p.cuts);
+        t = p.whole + (t - p.whole) / p.cuts;
+    }
     const int64_t per = static_cast<int64_t>(kPGroup) * p.ntiles;
     const int64_t group = t / per, first = group * kPGroup;
     const int64_t left = p.plan.units - first;
     const int h = static_cast<int>(left < kPGroup ? left : kPGroup);
     const int loc = static_cast<int>(t - group * per);
-    return {first + loc % h, (loc / h) * kPN};
+    return {first + loc % h, (loc / h) * kPN + piece * width, width};
 }
 
 template <bool B_MN>
 __global__ void __launch_bounds__(kPThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-            const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmE, const PairParams p) {
+            const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmE,
+            const __grid_constant__ CUtensorMap tmWp, const __grid_constant__ CUtensorMap tmEp, const PairParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -117,10 +127,15 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             int64_t issued = 0;
             bool ok = true, waited = false;
             const uint32_t eb = 256u * p.rpad;  // bytes of an adapter's columns, and of the rows' U
-            for (int64_t t = slot; t < p.tiles && ok; t += nslot) {
+            for (int64_t t = slot; t < p.items && ok; t += nslot) {
                 const PairTile ti = pair_tile(t, p);
+                if (ti.n0 >= p.ncols) continue;  // a piece past the last column
                 const int32_t arow = static_cast<int32_t>(ti.unit * kUnit + rank * kPM);
-                const int32_t nh = ti.n0 + static_cast<int32_t>(rank) * (kPN / 2);
+                const int half = ti.width / 2;  // columns of one CTA
+                const int32_t nh = ti.n0 + static_cast<int32_t>(rank) * half;
+                const bool whole = ti.width == kPN;
+                const CUtensorMap* mW = whole ? &tmW : &tmWp;
+                const CUtensorMap* mE = whole ? &tmE : &tmEp;
                 const int ne = p.plan.cnt[ti.unit];
                 const int32_t* gid = p.plan.gid + ti.unit * p.plan.slots;
                 for (int i = 0; i < nb; ++i) {
@@ -130,13 +145,13 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                     const uint32_t bar = mapa_u32(&ctl->full[stage], 0);
                     const int32_t red = i * kPK;
                     if (elect) {
-                        if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2 * kPStage);
+                        if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2u * (kPSlot + half * kPK * 2));
                         tma_load_2d_pair(sA, &tmX, bar, red, arow);
                         if (B_MN) {
-                            tma_load_2d_pair(sB, &tmW, bar, nh, red);
-                            tma_load_2d_pair(sB + 8192, &tmW, bar, nh + 64, red);
+                            tma_load_2d_pair(sB, mW, bar, nh, red);
+                            if (whole) tma_load_2d_pair(sB + 8192, mW, bar, nh + 64, red);
                         } else {
-                            tma_load_2d_pair(sB, &tmW, bar, red, nh);
+                            tma_load_2d_pair(sB, mW, bar, red, nh);
                         }
                     }
                     ++issued;
@@ -163,16 +178,16 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                     uint8_t* sB = sA + kPSlot;
                     const uint32_t bar = mapa_u32(&ctl->full[stage], 0);
                     if (elect) {
-                        if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2u * (eb + eb * en));
+                        if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2u * (eb + half * p.rpad * 2 * en));
                         tma_load_2d_pair(sA, &tmU, bar, rc, arow);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             if (e >= en) break;
                             if (B_MN) {
-                                tma_load_3d_pair(sB + e * eb, &tmE, bar, nh, rc, now[e]);
-                                tma_load_3d_pair(sB + e * eb + eb / 2, &tmE, bar, nh + 64, rc, now[e]);
+                                tma_load_3d_pair(sB + e * eb, mE, bar, nh, rc, now[e]);
+                                if (whole) tma_load_3d_pair(sB + e * eb + eb / 2, mE, bar, nh + 64, rc, now[e]);
                             } else {
-                                tma_load_3d_pair(sB + e * eb, &tmE, bar, rc, nh, now[e]);
+                                tma_load_3d_pair(sB + e * eb, mE, bar, rc, nh, now[e]);
                             }
                         }
                     }
@@ -195,7 +210,6 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
         // ----------------------------------------------------- MMA issuer --
         if (leader) {
             const bool elect = elect_one();
-            constexpr uint32_t idesc = idesc_bf16_f32(2 * kPM, kPN, 0, B_MN ? 1 : 0);
             // stage 0's operands: the shared product's, the adapters'
             const uint32_t eb = 256u * p.rpad;
             const Desc dX(smem_desc(ring0, 16, 1024, kLayoutSw128));
@@ -207,8 +221,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             int stage = 0;
             uint32_t phase = 0, acc = 0;
             bool ok = true, any_mma = false;
-            for (int64_t t = slot; t < p.tiles && ok; t += nslot, ++acc) {
+            for (int64_t t = slot; t < p.items && ok; t += nslot) {
                 const PairTile ti = pair_tile(t, p);
+                if (ti.n0 >= p.ncols) continue;
+                const uint32_t idesc = idesc_bf16_f32_n(2 * kPM, ti.width, 0, B_MN ? 1 : 0);
                 const int ne = p.plan.cnt[ti.unit];
                 const uint4* masks = reinterpret_cast<const uint4*>(p.plan.mask + ti.unit * p.plan.slots * kUnitWords);
                 // the rows of a block's adapters, loaded one block ahead (the first block's
@@ -266,6 +282,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                     if (++stage == kPStages) { stage = 0; phase ^= 1u; }
                 }
                 if (ok && elect) umma_commit_pair(&ctl->tmem_full[buf], 0x3);
+                ++acc;
             }
             if (any_mma) {
                 if (elect) umma_commit_pair(&ctl->drain, 0x1);
@@ -279,8 +296,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
         const int q = warp & 3;
         const uint64_t pol = l2_policy_evict_first();
         uint32_t acc = 0;
-        for (int64_t t = slot; t < p.tiles; t += nslot, ++acc) {
+        for (int64_t t = slot; t < p.items; t += nslot) {
             const PairTile ti = pair_tile(t, p);
+            if (ti.n0 >= p.ncols) continue;
+            const int end = min(p.ncols, ti.n0 + ti.width);
             const int64_t row = ti.unit * kUnit + rank * kPM + q * 32 + lane;
             uint16_t* orow = row < p.plan.T ? p.out + row * p.ncols : nullptr;
             const uint32_t buf = acc & 1u;
@@ -288,13 +307,13 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             tc_fence_after();
             const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * kPN;
 #pragma unroll 1
-            for (int c = 0; c < kPN; c += 128) {
+            for (int c = 0; c < ti.width; c += 128) {
                 __syncwarp();
                 uint32_t v[4][32];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(ta + c + 32 * k, v[k]);
                 tmem_ld_wait();
-                if (c + 128 == kPN) {
+                if (c + 128 >= ti.width) {
                     // every column is in registers: hand the accumulator back
                     tc_fence_before();
                     __syncwarp();
@@ -318,14 +337,15 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                                               pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
                                               pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
                         }
-                        if (p.st32 && col + 8 < p.ncols) {
+                        if (p.st32 && col + 8 < end) {
                             st_global_32_policy(orow + col, o[0], o[1], pol);
                         } else {
-                            if (col < p.ncols) st_global_16_policy(orow + col, o[0], pol);
-                            if (col + 8 < p.ncols) st_global_16_policy(orow + col + 8, o[1], pol);
+                            if (col < end) st_global_16_policy(orow + col, o[0], pol);
+                            if (col + 8 < end) st_global_16_policy(orow + col + 8, o[1], pol);
                         }
                     }
             }
+            ++acc;
         }
     }
 
@@ -346,12 +366,12 @@ int pair_room(int* clusters) {
     return rc;
 }
 
+// X, W, U, adapters; W's and the adapters' columns of a piece
 template <bool B_MN>
-int launch_pair(const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& u, const CUtensorMap& e,
-                const PairParams& p, int clusters, cudaStream_t st) {
-    ClusterLaunch l(2 * (p.tiles < clusters ? p.tiles : clusters), kPThreads, kPairSmem, 2, true, st);
+int launch_pair(const CUtensorMap (&m)[6], const PairParams& p, int clusters, cudaStream_t st) {
+    ClusterLaunch l(2 * (p.items < clusters ? p.items : clusters), kPThreads, kPairSmem, 2, true, st);
     clear_pending_launch_error();
-    const cudaError_t err = cudaLaunchKernelEx(&l.cfg, pair_kernel<B_MN>, x, w, u, e, p);
+    const cudaError_t err = cudaLaunchKernelEx(&l.cfg, pair_kernel<B_MN>, m[0], m[1], m[2], m[3], m[4], m[5], p);
     if (err != cudaSuccess) { record_cuda_error(err); return GG_ERR_CUDA; }
     return launch_result();
 }
@@ -372,21 +392,36 @@ int lora_pair_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const uint
     const int rc = b_mn ? pair_room<true>(&clusters) : pair_room<false>(&clusters);
     if (rc != GG_OK) return rc;
     p.ntiles = static_cast<int>((ncols + kPN - 1) / kPN);
-    p.tiles = plan.units * p.ntiles;
+    // The last round's tiles, if they are at most half of the clusters, in halves: a round
+    // takes as long as its widest item (2600 rows of 4096 x 2056: 52 us whole, 45 cut; in
+    // quarters, whose blocks are bound by their row loads, no less).
+    const int64_t tiles = plan.units * p.ntiles, rest = tiles % clusters;
+    p.cuts = rest * 2 <= clusters ? 2 : 1;
+    p.whole = tiles - rest;
+    p.items = p.whole + rest * p.cuts;
     p.out = out;
     p.st32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && ncols % 16 == 0;
     p.status = status;
-    CUtensorMap mX{}, mW{}, mU{}, mE{};
-    if (!encode_map_2d(&mX, X, Kred, plan.T, Kred, kPK, kPM)) return GG_ERR_CUDA;
-    if (!encode_map_2d(&mU, U, r, plan.T, r, p.rpad, kPM)) return GG_ERR_CUDA;
-    if (b_mn) {  // W [Kred, ncols], ad [L, r, ncols]
-        if (!encode_map_2d(&mW, W, ncols, Kred, ncols, 64, kPK)) return GG_ERR_CUDA;
-        if (!encode_map_3d(&mE, ad, ncols, r, plan.L, ncols, ncols * r, 64, p.rpad)) return GG_ERR_CUDA;
-        return launch_pair<true>(mX, mW, mU, mE, p, clusters, st);
+    CUtensorMap m[6] = {};
+    if (!encode_map_2d(&m[0], X, Kred, plan.T, Kred, kPK, kPM)) return GG_ERR_CUDA;
+    if (!encode_map_2d(&m[2], U, r, plan.T, r, p.rpad, kPM)) return GG_ERR_CUDA;
+    if (b_mn) {  // W [Kred, ncols], ad [L, r, ncols]: 64-column pieces in either case
+        if (!encode_map_2d(&m[1], W, ncols, Kred, ncols, 64, kPK)) return GG_ERR_CUDA;
+        if (!encode_map_3d(&m[3], ad, ncols, r, plan.L, ncols, ncols * r, 64, p.rpad)) return GG_ERR_CUDA;
+        m[4] = m[1];
+        m[5] = m[3];
+        return launch_pair<true>(m, p, clusters, st);
     }
-    if (!encode_map_2d(&mW, W, Kred, ncols, Kred, kPK, kPN / 2)) return GG_ERR_CUDA;
-    if (!encode_map_3d(&mE, ad, r, ncols, plan.L, r, ncols * r, p.rpad, kPN / 2)) return GG_ERR_CUDA;
-    return launch_pair<false>(mX, mW, mU, mE, p, clusters, st);
+    if (!encode_map_2d(&m[1], W, Kred, ncols, Kred, kPK, kPN / 2)) return GG_ERR_CUDA;
+    if (!encode_map_3d(&m[3], ad, r, ncols, plan.L, r, ncols * r, p.rpad, kPN / 2)) return GG_ERR_CUDA;
+    m[4] = m[1];
+    m[5] = m[3];
+    if (p.cuts > 1 && rest > 0) {
+        const uint32_t half = kPN / 2 / p.cuts;
+        if (!encode_map_2d(&m[4], W, Kred, ncols, Kred, kPK, half)) return GG_ERR_CUDA;
+        if (!encode_map_3d(&m[5], ad, r, ncols, plan.L, r, ncols * r, p.rpad, half)) return GG_ERR_CUDA;
+    }
+    return launch_pair<false>(m, p, clusters, st);
 }
 
 }  // namespace gg
