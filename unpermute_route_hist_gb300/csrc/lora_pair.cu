@@ -11,6 +11,10 @@
 // Sorting rows by adapter instead would read and write X and Y once more, or
 // gather X (2.5x slower loads here), and break tiles at every adapter's end.
 //
+// An adapter block costs about a shared one (471 cycles): its adapters' ids and row masks
+// wait in shared memory, copied while the shared blocks run (read from global memory a
+// block ahead they took 977).
+//
 // Warp 0: TMA producer; warp 1: tensor memory and, in the even CTA, MMA issue;
 // warps 2-5: epilogue (tensor memory -> bf16 -> 32-byte row pieces).  Every wait
 // is bounded (GG_DEV_TIMEOUT).
@@ -46,6 +50,8 @@ struct PairCtl {
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
+    alignas(16) uint32_t mask[kUnit][kUnitWords];  // the issuer's tile: rows of each entry
+    int32_t gid[kUnit];                            // the producer's tile: its adapters
 };
 constexpr int kPairSmem = 1024 + kPStages * kPStage + sizeof(PairCtl);
 
@@ -138,6 +144,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                 const CUtensorMap* mE = whole ? &tmE : &tmEp;
                 const int ne = p.plan.cnt[ti.unit];
                 const int32_t* gid = p.plan.gid + ti.unit * p.plan.slots;
+                const int fetch_at = min(nb, kPStages) - 1;  // with the ring full of loads
                 for (int i = 0; i < nb; ++i) {
                     if (!all_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
                     uint8_t* sA = ring + stage * kPStage;
@@ -154,24 +161,21 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                             tma_load_2d_pair(sB, mW, bar, red, nh);
                         }
                     }
+                    if (i == fetch_at) {
+                        for (int e = lane; e < ne; e += 32)
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&ctl->gid[e])), "l"(gid + e) : "memory");
+                        cp_async_commit();
+                    }
                     ++issued;
                     if (++stage == kPStages) { stage = 0; phase ^= 1u; }
                 }
                 if (!ok) break;
                 const int xb = ext_blocks(ne);
-                int32_t g[4] = {0, 0, 0, 0};  // a block's adapters, loaded one block ahead
-                auto load_ids = [&](int xi) {
-                    const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (e < p.epb && ef + e < ne) g[e] = gid[ef + e];
-                };
-                if (xb > 0) load_ids(0);
+                cp_async_wait<0>();
+                __syncwarp();
+                int ef = 0, rc = 0;  // first entry of the block, its rank columns
                 for (int xi = 0; xi < xb; ++xi) {
-                    const int en = p.r <= 64 ? min(p.epb, ne - xi * p.epb) : 1;
-                    const int rc = p.r <= 64 ? 0 : (xi % rchunks) * 64;
-                    const int32_t now[4] = {g[0], g[1], g[2], g[3]};
-                    if (xi + 1 < xb) load_ids(xi + 1);
+                    const int en = min(p.epb, ne - ef);
                     if (!all_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
                     if (!waited) { pdl_wait(); waited = true; }  // U (V) of the kernel before
                     uint8_t* sA = ring + stage * kPStage;
@@ -184,16 +188,21 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                         for (int e = 0; e < 4; ++e) {
                             if (e >= en) break;
                             if (B_MN) {
-                                tma_load_3d_pair(sB + e * eb, mE, bar, nh, rc, now[e]);
-                                if (whole) tma_load_3d_pair(sB + e * eb + eb / 2, mE, bar, nh + 64, rc, now[e]);
+                                tma_load_3d_pair(sB + e * eb, mE, bar, nh, rc, ctl->gid[ef + e]);
+                                if (whole) tma_load_3d_pair(sB + e * eb + eb / 2, mE, bar, nh + 64, rc, ctl->gid[ef + e]);
                             } else {
-                                tma_load_3d_pair(sB + e * eb, mE, bar, rc, nh, now[e]);
+                                tma_load_3d_pair(sB + e * eb, mE, bar, rc, nh, ctl->gid[ef + e]);
                             }
                         }
+                    }
+                    if ((rc += 64) >= p.r) {
+                        rc = 0;
+                        ef += p.epb;
                     }
                     ++issued;
                     if (++stage == kPStages) { stage = 0; phase ^= 1u; }
                 }
+                __syncwarp();  // every lane has read its ids before the next tile's arrive
             }
             if (!waited) pdl_wait();  // the launch before this one has finished before this grid can
             // The even CTA's barriers count both CTAs' copies: let them land.
@@ -227,19 +236,6 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                 const uint32_t idesc = idesc_bf16_f32_n(2 * kPM, ti.width, 0, B_MN ? 1 : 0);
                 const int ne = p.plan.cnt[ti.unit];
                 const uint4* masks = reinterpret_cast<const uint4*>(p.plan.mask + ti.unit * p.plan.slots * kUnitWords);
-                // the rows of a block's adapters, loaded one block ahead (the first block's
-                // with the shared product's still to come)
-                uint4 m[4][2];
-                auto load_masks = [&](int xi) {
-                    const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (e >= p.epb || ef + e >= ne) continue;
-                        m[e][0] = __ldg(masks + 2 * (ef + e));
-                        m[e][1] = __ldg(masks + 2 * (ef + e) + 1);
-                    }
-                };
-                load_masks(0);
                 const uint32_t buf = acc & 1u;
                 if (!all_wait(&ctl->tmem_empty[buf], ((acc >> 1) & 1u) ^ 1u, abort_flag, p.status, true)) break;
                 tc_fence_after();
@@ -254,14 +250,21 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                             umma_at<true>(d, dX, at + 2 * ks, dW, at + kStep * ks, idesc, (i > 0 || ks > 0) ? 1u : 0u);
                         umma_commit_pair(&ctl->empty[stage], 0x3);
                     }
+                    if (i == 0) {  // the masks, while the shared product runs
+                        for (int e = lane; e < 2 * ne; e += 32)
+                            cp_async_16(smem_u32(&ctl->mask[0][0]) + 16 * e, masks + e, 16u);
+                        cp_async_commit();
+                    }
                     any_mma = true;
                     if (++stage == kPStages) { stage = 0; phase ^= 1u; }
                 }
                 const int xb = ext_blocks(ne);
+                cp_async_wait<0>();
+                __syncwarp();
+                int ef = 0, rc = 0;
                 for (int xi = 0; xi < xb && ok; ++xi) {
-                    const int en = p.r <= 64 ? min(p.epb, ne - xi * p.epb) : 1;
-                    const int left = p.r <= 64 ? p.r : min(64, p.r - (xi % rchunks) * 64);
-                    const int steps = (left + 15) / 16;
+                    const int en = min(p.epb, ne - ef);
+                    const int steps = (min(64, p.r - rc) + 15) / 16;
                     if (!all_wait(&ctl->full[stage], phase, abort_flag, p.status)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t at = stage * (kPStage / 16);
@@ -269,8 +272,9 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             if (e >= en) break;
-                            const uint32_t keep[8] = {m[e][0].x, m[e][0].y, m[e][0].z, m[e][0].w,
-                                                      m[e][1].x, m[e][1].y, m[e][1].z, m[e][1].w};
+                            const uint4 m0 = *reinterpret_cast<const uint4*>(&ctl->mask[ef + e][0]);
+                            const uint4 m1 = *reinterpret_cast<const uint4*>(&ctl->mask[ef + e][4]);
+                            const uint32_t keep[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
                                 if (ks < steps)
@@ -278,9 +282,13 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                         }
                         umma_commit_pair(&ctl->empty[stage], 0x3);
                     }
-                    if (xi + 1 < xb) load_masks(xi + 1);
+                    if ((rc += 64) >= p.r) {
+                        rc = 0;
+                        ef += p.epb;
+                    }
                     if (++stage == kPStages) { stage = 0; phase ^= 1u; }
                 }
+                __syncwarp();  // every mask has been read before the next tile's arrive
                 if (ok && elect) umma_commit_pair(&ctl->tmem_full[buf], 0x3);
                 ++acc;
             }

@@ -46,7 +46,7 @@ struct ProjectCtl {
     int abort_flag;
     int nent;                   // adapters that occur in this row tile
     int32_t gid[kRM];
-    uint32_t mask[kRM][4];
+    alignas(16) uint32_t mask[kRM][4];
 };
 
 constexpr int kProjectSmem = 1024 + kRRing + 4096;
@@ -149,6 +149,14 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     const uint32_t tmem = ctl->tmem_base;
     const uint32_t ring0 = smem_u32(ring);
     const uint32_t eb = 256u * p.rpad;  // bytes of an adapter's columns in a stage
+    // the first adapter block's entry and rank columns; the next block's
+    const int ef0 = p.r <= 64 ? x_lo * p.epb : x_lo / rchunks, rc0 = p.r <= 64 ? 0 : (x_lo % rchunks) * 64;
+    auto next_block = [&](int& ef, int& rc) {
+        if ((rc += 64) >= p.r) {
+            rc = 0;
+            ef += p.epb;
+        }
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------- producer --
@@ -156,6 +164,7 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         int issued = min(nbase, stages);
         int stage = issued % stages;
         uint32_t phase = issued == stages ? 1u : 0u;
+        int ef = ef0, rc = rc0;
         bool waited = false;
         for (int i = issued; i < nblk; ++i) {
             if (!all_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) break;
@@ -166,10 +175,7 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 uint8_t* sA = ring + stage * stage_bytes;
                 uint8_t* sB = sA + a_slot;
                 uint64_t* bar = &ctl->full[stage];
-                const int xi = x_lo + i - nbase;
-                const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
-                const int en = p.r <= 64 ? min(p.epb, ne - ef) : 1;
-                const int rc = p.r <= 64 ? 0 : (xi % rchunks) * 64;
+                const int en = min(p.epb, ne - ef);
                 if (elect) {
                     mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.xrows) * p.rpad * 2u + eb * en);
                     tma_load_2d(sA, &tmU, bar, rc, static_cast<int32_t>(row0));
@@ -183,6 +189,7 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                         }
                     }
                 }
+                next_block(ef, rc);
             }
             ++issued;
             if (++stage == stages) { stage = 0; phase ^= 1u; }
@@ -208,6 +215,7 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         const Desc dU(kmajor_desc(ring0, p.rpad * 2));
         const Desc dE(B_MN ? smem_desc(ring0 + a_slot, eb / 2, 1024, kLayoutSw128) : kmajor_desc(ring0 + a_slot, p.rpad * 2));
         constexpr uint32_t kStep = B_MN ? 128 : 2;  // 16 reduction columns of the right operand
+        int ef = ef0, rc = rc0;
         for (int i = 0; i < nblk; ++i) {
             if (!all_wait(&ctl->full[stage], phase, abort_flag, p.status)) break;
             tc_fence_after();
@@ -219,21 +227,21 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                         umma_at<false>(tmem, dX, at + 2 * ks, dW, at + kStep * ks, idesc, (i > 0 || ks > 0) ? 1u : 0u);
                 }
             } else {
-                const int xi = x_lo + i - nbase;
-                const int ef = p.r <= 64 ? xi * p.epb : xi / rchunks;
-                const int en = p.r <= 64 ? min(p.epb, ne - ef) : 1;
-                const int left = p.r <= 64 ? p.r : min(64, p.r - (xi % rchunks) * 64);
-                const int steps = (left + 15) / 16;
-                for (int e = 0; e < en; ++e) {
-                    const uint32_t keep[4] = {ctl->mask[ef + e][0], ctl->mask[ef + e][1], ctl->mask[ef + e][2],
-                                              ctl->mask[ef + e][3]};
-                    if (elect) {
+                const int en = min(p.epb, ne - ef);
+                const int steps = (min(64, p.r - rc) + 15) / 16;
+                if (elect) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (e >= en) break;
+                        const uint4 m = *reinterpret_cast<const uint4*>(&ctl->mask[ef + e][0]);
+                        const uint32_t keep[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             if (ks < steps)
                                 umma_rows_at(tmem, dU, at + 2 * ks, dE, at + e * (eb / 16) + kStep * ks, idesc, keep);
                     }
                 }
+                next_block(ef, rc);
             }
             if (elect) umma_commit(&ctl->empty[stage]);
             any_mma = true;
