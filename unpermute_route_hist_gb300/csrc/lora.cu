@@ -120,7 +120,8 @@ int gg_lora_backward(const gg_bf16* dY, const gg_bf16* X, const gg_bf16* W, cons
         e = cuda_result(cudaMemsetAsync(counters, 0, kGradCtas * sizeof(uint32_t), st));
     if (e == GG_OK && dX) e = project(true, dY, W, V, A, v, N, K, r, dX, status, st);
     if (e == GG_OK && (dA || dB))
-        e = lora_grad_launch(X, dY, U, V, V_lo, v, K, N, r, dA, dB, counters, sums, status, st);
+        e = lora_grad_launch(X, dY, U, V, V_lo, v, K, N, r, dA, dB, counters, sums,
+                             dX ? GRAD_AFTER_DX : (dA ? GRAD_AFTER_V : GRAD_AFTER_OTHER), status, st);
     return e;
 }
 

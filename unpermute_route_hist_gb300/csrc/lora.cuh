@@ -325,9 +325,11 @@ int lora_pair_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const uint
 // dA, dB (either may be null); counters: kGradCtas zeroed words, sums: the CTAs' partial
 // sums, 2 x kGradCtas x 128 x r floats.
 constexpr int kGradCtas = 320;
+// What was launched just before: V's kernel, dX's (itself after V's), or something else.
+enum GradAfter { GRAD_AFTER_V, GRAD_AFTER_DX, GRAD_AFTER_OTHER };
 int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, const uint16_t* V, const uint16_t* V_lo,
                      const PlanView& plan, int64_t K, int64_t N, int r, uint16_t* dA, uint16_t* dB, uint32_t* counters,
-                     float* sums, int32_t* status, cudaStream_t st);
+                     float* sums, GradAfter after, int32_t* status, cudaStream_t st);
 int lora_plan_launch(const int32_t* ids, const PlanView& plan, int32_t* status, cudaStream_t st);
 
 }  // namespace gg

@@ -48,6 +48,7 @@ struct GradParams {
     int stage_bytes;
     uint32_t* counter;         // [CTA]: arrivals of the item that CTA began and did not end
     float* sums;               // [CTA][2][r][128]
+    int after_v;               // follows the kernel that writes V and clears the counters
     int32_t* status;
 };
 
@@ -108,6 +109,10 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
     const int buf_cols = ncols <= 16 ? 16 : (ncols <= 32 ? 32 : (ncols <= 64 ? 64 : (ncols <= 128 ? 128 : 256)));
     constexpr uint32_t piece_bytes = CHUNK * kGK * 2;
 
+    // Launched while the kernel before runs.  That is the one that makes V, to be waited
+    // for, or dX's, which lets this grid start only once V is complete: then nothing here
+    // depends on it, and these CTAs fill the SMs its last tiles leave idle.
+    if (p.after_v) pdl_wait();
     // adapters without tokens get zeros, a piece from every CTA: a lane looks at an
     // adapter, the warp clears those found
     for (int a0 = warp * 32; a0 < p.plan.L; a0 += kGThreads) {
@@ -129,7 +134,10 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
     // the CTAs that share the list: none without a block, else kGMinBlocks each
     const int64_t fit = total / kGMinBlocks > 1 ? total / kGMinBlocks : 1;
     const int64_t G = fit < gridDim.x ? fit : gridDim.x;
-    if (blockIdx.x >= G) return;
+    if (blockIdx.x >= G) {
+        pdl_wait();
+        return;
+    }
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -478,6 +486,7 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
         }
     }
 
+    pdl_wait();  // this grid does not end before the one before it
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -487,7 +496,7 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
 }
 
 template <int RING, int CTAS, int CHUNK>
-int launch_grad(const GradMaps& m, GradParams p, cudaStream_t st) {
+int launch_grad(const GradMaps& m, GradParams p, bool after_kernel, cudaStream_t st) {
     constexpr size_t smem = 1024 + RING;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -504,8 +513,10 @@ int launch_grad(const GradMaps& m, GradParams p, cudaStream_t st) {
     if (p.stages > kGMaxStages) p.stages = kGMaxStages;
     int64_t G = int64_t(CTAS) * num_sms();  // every CTA resident at once
     if (G > kGradCtas) G = kGradCtas;
+    ClusterLaunch l(G, kGThreads, smem, 1, after_kernel, st);
     clear_pending_launch_error();
-    grad_kernel<RING, CTAS, CHUNK><<<static_cast<unsigned>(G), kGThreads, smem, st>>>(m, p);
+    e = cudaLaunchKernelEx(&l.cfg, grad_kernel<RING, CTAS, CHUNK>, m, p);
+    if (e != cudaSuccess) { record_cuda_error(e); return GG_ERR_CUDA; }
     return launch_result();
 }
 
@@ -513,8 +524,10 @@ int launch_grad(const GradMaps& m, GradParams p, cudaStream_t st) {
 
 int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, const uint16_t* V, const uint16_t* V_lo,
                      const PlanView& plan, int64_t K, int64_t N, int r, uint16_t* dA, uint16_t* dB, uint32_t* counters,
-                     float* sums, int32_t* status, cudaStream_t st) {
+                     float* sums, GradAfter after, int32_t* status, cudaStream_t st) {
     GradParams p{};
+    p.after_v = after == GRAD_AFTER_V;
+    const bool kernel = after != GRAD_AFTER_OTHER;
     p.plan = plan;
     p.r = r;
     const int chunk = rank_pad(r);
@@ -538,9 +551,9 @@ int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, c
         if (!encode_map_2d(&m.narrow[2], U, r, plan.T, r, chunk, kGK)) return GG_ERR_CUDA;
     }
     // two CTAs an SM for ranks up to 64, one above
-    if (chunk == 16) return launch_grad<98304, 2, 16>(m, p, st);
-    if (chunk == 32) return launch_grad<98304, 2, 32>(m, p, st);
-    return p.nc == 1 ? launch_grad<98304, 2, 64>(m, p, st) : launch_grad<196608, 1, 64>(m, p, st);
+    if (chunk == 16) return launch_grad<98304, 2, 16>(m, p, kernel, st);
+    if (chunk == 32) return launch_grad<98304, 2, 32>(m, p, kernel, st);
+    return p.nc == 1 ? launch_grad<98304, 2, 64>(m, p, kernel, st) : launch_grad<196608, 1, 64>(m, p, kernel, st);
 }
 
 }  // namespace gg

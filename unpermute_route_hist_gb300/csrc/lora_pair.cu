@@ -177,7 +177,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                 for (int xi = 0; xi < xb; ++xi) {
                     const int en = min(p.epb, ne - ef);
                     if (!all_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
-                    if (!waited) { pdl_wait(); waited = true; }  // U (V) of the kernel before
+                    if (!waited) {
+                        pdl_wait();  // U (V) of the kernel before
+                        waited = true;
+                        pdl_launch_dependents();  // (the next kernel may read it too)
+                    }
                     uint8_t* sA = ring + stage * kPStage;
                     uint8_t* sB = sA + kPSlot;
                     const uint32_t bar = mapa_u32(&ctl->full[stage], 0);
@@ -204,7 +208,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                 }
                 __syncwarp();  // every lane has read its ids before the next tile's arrive
             }
-            if (!waited) pdl_wait();  // the launch before this one has finished before this grid can
+            if (!waited) {
+                pdl_wait();  // the launch before this one has finished before this grid can
+                pdl_launch_dependents();
+            }
             // The even CTA's barriers count both CTAs' copies: let them land.
             if (leader) {
                 const int64_t pend = issued < kPStages ? issued : kPStages;

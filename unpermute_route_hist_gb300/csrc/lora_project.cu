@@ -171,7 +171,11 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             if (i < nbase) {
                 if (elect) load_base(i, stage);
             } else {
-                if (!waited) { pdl_wait(); waited = true; }  // U (V) of the kernel before
+                if (!waited) {
+                    pdl_wait();  // U (V) of the kernel before
+                    waited = true;
+                    pdl_launch_dependents();  // (the next kernel may read it too)
+                }
                 uint8_t* sA = ring + stage * stage_bytes;
                 uint8_t* sB = sA + a_slot;
                 uint64_t* bar = &ctl->full[stage];
@@ -194,7 +198,10 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             ++issued;
             if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
-        if (!waited) pdl_wait();  // the launch before this one has finished before this grid can
+        if (!waited) {
+            pdl_wait();  // the launch before this one has finished before this grid can
+            pdl_launch_dependents();
+        }
         // every copy has landed before the ring is reused or the CTA exits
         for (int j = 0; j < min(issued, stages); ++j) {
             if (--stage < 0) { stage = stages - 1; phase ^= 1u; }
