@@ -343,3 +343,30 @@ def test_refusals(gg):
     with pytest.raises(gg.GGError):
         gg.lora_backward(g["dY"], *ok, torch.zeros(16, 8, dtype=torch.bfloat16, device=dev()),
                          workspace=torch.empty(16, dtype=torch.uint8, device=dev()))
+
+
+@pytest.mark.parametrize("T,r", [(1, 8), (31, 24), (300, 256), (777, 16), (2049, 136), (5000, 64)])
+@pytest.mark.parametrize("order", ["all", "first half", "every third", "all but the last"])
+def test_rows_without_an_adapter_in_dirty_memory(gg, T, r, order):
+    """U of a row without an adapter is zero whatever stood there, its Y and dX are the shared
+    product's alone, and a backward in a dirty workspace gives finite sums."""
+    K, N, L = 136, 72, 3
+    d = make(T, K, N, L, r, "runs", seed=T + r)
+    ids, at = np.sort(d["ids"] % L), np.arange(T)
+    bare = {"all": at >= 0, "first half": at < T // 2, "every third": at % 3 == 0, "all but the last": at < T - 1}[order]
+    d["ids"] = np.where(bare, -1, ids).astype(np.int32)
+    g, st = on_gpu(d), status_tensor()
+    plan = gg.lora_plan(g["ids"], L, status=st)
+    dirty = lambda *s: torch.full(s, float("nan"), dtype=torch.bfloat16, device=dev())
+    Y, U = gg.lora_forward(g["X"], g["W"], g["A"], g["B"], g["scale"], plan, out=dirty(T, N), out_u=dirty(T, r), status=st)
+    ref, refu, bound, boundu = forward_ref(d)
+    within(U, refu, boundu, "U")
+    within(Y, ref, bound, "Y")
+    assert not U[torch.from_numpy(bare).to(dev())].any()
+    ws = torch.full((gg.lora_backward_workspace_size(T, r),), 255, dtype=torch.uint8, device=dev())
+    got = gg.lora_backward(g["dY"], g["X"], g["W"], g["A"], g["B"], g["scale"], plan, U, out=dirty(T, K),
+                           out_da=dirty(L, r, K), out_db=dirty(L, N, r), workspace=ws, status=st)
+    assert status_of(st) == 0
+    ref = backward_ref(d, get(U))
+    for i, what in enumerate(("dX", "dA", "dB")):
+        within(got[i], ref[i], ref[3 + i], what)
