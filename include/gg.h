@@ -410,8 +410,9 @@ int gg_ep_recv_map(const int32_t* recv_m, int G, int E_loc, int64_t R_loc, int32
  *  GG_LORA_MAX_RANK (a smaller rank is zero-padded by the caller); N, K
  *  multiples of 8; L <= GG_MAX_EXPERTS.  A row is computed from its own adapter
  *  alone: infinities or NaN in one adapter or row reach no other row.
- *  U is kept for the backward (needed by it alone).  No counterpart on the
- *  pages.
+ *  U is kept for the backward (needed by it alone).  Outputs (here and in the
+ *  backward) overlap neither inputs nor one another: kernels of a call run side
+ *  by side.  No counterpart on the pages.
  *
  * gg_lora_plan reads a batch's ids once: the adapters that occur in each 256
  * rows, as row masks, and the rows sorted by adapter, into a buffer of
@@ -434,7 +435,7 @@ int gg_lora_forward(const gg_bf16* X, const gg_bf16* W, const gg_bf16* A, const 
  *  each may be NULL (not computed; its operands may then be NULL too: X for dA,
  *  U for dB, W and A for dX).  An adapter without tokens gets zeros.
  *  workspace: gg_lora_backward_workspace_size(T, r) bytes, 16-byte aligned
- *  (needed for dX and dA).  Deterministic (fixed reduction orders). */
+ *  (whichever gradients are wanted).  Deterministic (fixed reduction orders). */
 size_t gg_lora_backward_workspace_size(int64_t T, int r);
 int gg_lora_backward(const gg_bf16* dY, const gg_bf16* X, const gg_bf16* W, const gg_bf16* A,
                      const gg_bf16* B, const float* scale, const void* plan, const gg_bf16* U,

@@ -195,3 +195,18 @@ def test_empty_and_refusals(gg):
     big = gg.rope_freqs(2048, device=dev())
     with pytest.raises(gg.GGError):
         gg.rope(torch.zeros(1, 1, 2048, dtype=torch.bfloat16, device=dev()), None, pos[:1], big)
+
+
+def test_offsets_past_32_bits(gg):
+    """The last heads of a packed projection of more than 2^31 elements, in place: the bits of
+    the same rows by themselves, and nothing beside them changes."""
+    T, width, H, D, last = 360000, 6144, 2, 128, 300
+    buf = torch.zeros(T, width, dtype=torch.bfloat16, device=dev())
+    buf[-last:] = torch.randn(last, width, device=dev())
+    tail = buf[-last:].clone()
+    heads = lambda x: x[:, width - H * D:].view(x.shape[0], H, D)
+    pos, freqs = torch.arange(T, dtype=torch.int32, device=dev()), gg.rope_freqs(D, device=dev())
+    for step in (gg.rope, gg.rope_bwd):
+        step(heads(buf), None, pos, freqs, out_q=heads(buf))
+        step(heads(tail), None, pos[-last:].clone(), freqs, out_q=heads(tail))
+        assert torch.equal(buf[-last:], tail) and not buf[:last].any()

@@ -24,10 +24,12 @@ size_t v_bytes(int64_t T, int r) { return (static_cast<size_t>(T) * r * 2 + 255)
 constexpr size_t kCounterBytes = (kGradCtas * sizeof(uint32_t) + 255) / 256 * 256;
 
 // Y (or dX) from its operands: tiles with a split reduction, or 2-CTA tiles.  Splitting
-// pays for few rows (64 of 4096 x 4096: 18 and 25 us; of 2048 x 2048: 14 both), and for
-// a long reduction, the adapters' blocks among it, whose 2-CTA tiles leave half of the
-// GPU idle (300 rows of 4096 x 4096, 4 adapters: 24 and 27; of 2048 x 2048, 16 mixed
-// adapters of rank 64: 19 and 24; 4 adapters: 19 and 16).
+// pays for few rows (whole forwards, split and 2-CTA: 64 rows of 4096 x 4096 18.8 and
+// 20.7 us; 48 of 2048 x 2048, 32 mixed adapters 12.7 and 17.5; it loses at 64 rows of
+// 2048 x 2048 in runs, 13.5 and 12.0), and for a long reduction, the adapters' blocks among
+// it, whose 2-CTA tiles leave half of the GPU idle (300 rows of 4096 x 4096, 4 adapters:
+// 23.5 and 25.9; of 2048 x 2048, 16 mixed adapters of rank 64: 18.2 and 20.7; 512 mixed
+// rows, 32 adapters of rank 128: 33.9 and 45.9; with 4 adapters of few blocks 19 and 16).
 int project(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, const uint16_t* ad,
             const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, int32_t* status, cudaStream_t st) {
     const int64_t pairs = plan.units * ((ncols + 255) / 256);

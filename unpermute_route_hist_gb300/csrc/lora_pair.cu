@@ -15,6 +15,9 @@
 // wait in shared memory, copied while the shared blocks run (read from global memory a
 // block ahead they took 977).
 //
+// 8192 rows of 4096 -> 6144 at rank 32, with the low-rank product before it: 229 us, 1.83
+// PFLOP/s; the tensor pipe is active 88% of this kernel's time.
+//
 // Warp 0: TMA producer; warp 1: tensor memory and, in the even CTA, MMA issue;
 // warps 2-5: epilogue (tensor memory -> bf16 -> 32-byte row pieces).  Every wait
 // is bounded (GG_DEV_TIMEOUT).

@@ -4,6 +4,10 @@
 // by every projection of every layer.  The result is the same on every run: an
 // entry's place is the rank of its adapter id in the unit's bitmap, a row's place
 // the rank of its bit, no atomic hands out places.
+//
+// Bound by launches: up to 256 rows one CTA does everything in one launch (13 us a
+// call from Python), more take five (22 us at 8192 rows), whose grids of one CTA a
+// unit read the ids once each.
 #include "lora.cuh"
 
 namespace gg {
