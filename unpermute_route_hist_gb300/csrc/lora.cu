@@ -21,7 +21,7 @@ int check_sizes(int64_t T, int L, int r, int64_t N, int64_t K) {
 
 // The backward's workspace: V, its remainder, the gradients' counters and partial sums.
 size_t v_bytes(int64_t T, int r) { return (static_cast<size_t>(T) * r * 2 + 255) / 256 * 256; }
-constexpr size_t kCounterBytes = (kGradCtas * sizeof(uint32_t) + 255) / 256 * 256;
+constexpr size_t kCounterBytes = (kGradWords * sizeof(uint32_t) + 255) / 256 * 256;
 
 // Y (or dX) from its operands: tiles with a split reduction, or 2-CTA tiles.  Splitting
 // pays for few rows (whole forwards, split and 2-CTA: 64 rows of 4096 x 4096 18.8 and
@@ -31,7 +31,8 @@ constexpr size_t kCounterBytes = (kGradCtas * sizeof(uint32_t) + 255) / 256 * 25
 // 23.5 and 25.9; of 2048 x 2048, 16 mixed adapters of rank 64: 18.2 and 20.7; 512 mixed
 // rows, 32 adapters of rank 128: 33.9 and 45.9; with 4 adapters of few blocks 19 and 16).
 int project(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, const uint16_t* ad,
-            const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, int32_t* status, cudaStream_t st) {
+            const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, uint32_t* ready, int32_t* status,
+            cudaStream_t st) {
     const int64_t pairs = plan.units * ((ncols + 255) / 256);
     // reduction blocks of a tile, with those of the adapters that can occur in it
     const int64_t rchunks = (r + 63) / 64, per = 64 / rank_pad(r);
@@ -39,8 +40,8 @@ int project(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, 
     const int64_t adapters = (plan.L < rows ? plan.L : rows) * rchunks / per;
     const int64_t blocks = (Kred + 63) / 64 + adapters;
     if (plan.T <= 64 || (pairs * 4 < num_sms() && blocks > 44))
-        return lora_project_launch(b_mn, X, W, U, ad, plan, Kred, ncols, r, out, status, st);
-    return lora_pair_launch(b_mn, X, W, U, ad, plan, Kred, ncols, r, out, status, st);
+        return lora_project_launch(b_mn, X, W, U, ad, plan, Kred, ncols, r, out, ready, status, st);
+    return lora_pair_launch(b_mn, X, W, U, ad, plan, Kred, ncols, r, out, ready, status, st);
 }
 
 }  // namespace
@@ -80,7 +81,7 @@ int gg_lora_forward(const gg_bf16* X, const gg_bf16* W, const gg_bf16* A, const 
     const PlanView v = plan_view(const_cast<void*>(plan), T, L);
     const int e = lora_shrink_launch(false, X, A, scale, v, K, r, U, nullptr, nullptr, 0, status, st);
     if (e != GG_OK || N == 0) return e;
-    return project(false, X, W, U, B, v, K, N, r, Y, status, st);
+    return project(false, X, W, U, B, v, K, N, r, Y, nullptr, status, st);
 }
 
 size_t gg_lora_backward_workspace_size(int64_t T, int r) {
@@ -117,10 +118,10 @@ int gg_lora_backward(const gg_bf16* dY, const gg_bf16* X, const gg_bf16* W, cons
     float* sums = reinterpret_cast<float*>(ws + 2 * v_bytes(T, r) + kCounterBytes);
     int e;
     if (dX || dA)
-        e = lora_shrink_launch(true, dY, B, scale, v, N, r, V, dA ? V_lo : nullptr, counters, kGradCtas, status, st);
+        e = lora_shrink_launch(true, dY, B, scale, v, N, r, V, dA ? V_lo : nullptr, counters, kGradWords, status, st);
     else
-        e = cuda_result(cudaMemsetAsync(counters, 0, kGradCtas * sizeof(uint32_t), st));
-    if (e == GG_OK && dX) e = project(true, dY, W, V, A, v, N, K, r, dX, status, st);
+        e = cuda_result(cudaMemsetAsync(counters, 0, kGradWords * sizeof(uint32_t), st));
+    if (e == GG_OK && dX) e = project(true, dY, W, V, A, v, N, K, r, dX, dA || dB ? counters + kGradCtas : nullptr, status, st);
     if (e == GG_OK && (dA || dB))
         e = lora_grad_launch(X, dY, U, V, V_lo, v, K, N, r, dA, dB, counters, sums,
                              dX ? GRAD_AFTER_DX : (dA ? GRAD_AFTER_V : GRAD_AFTER_OTHER), status, st);

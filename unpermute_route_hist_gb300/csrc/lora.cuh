@@ -209,13 +209,37 @@ __device__ __forceinline__ uint32_t mapa_addr(uint32_t addr, uint32_t cta) {
     return remote;
 }
 
+// This thread's reads through the async proxy (TMA) come after what is visible to it here.
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
 // Programmatic dependent launch: let the next kernel of the stream start its
 // prologue; wait until the previous one has finished and its writes are visible
 // (at once when this kernel was launched without the attribute).
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("fence.proxy.async;" ::: "memory");  // its stores, before this thread's TMA reads of them
+    fence_proxy_async();  // its stores, before this thread's TMA reads of them
+}
+
+// A kernel started beside the one before it (dX's) that reads what the launch before that
+// one wrote (V): the launch order starts it late enough, but only griddepcontrol.wait or a
+// release it has acquired makes the writes visible, and the wait would last until dX's end.
+// So dX's kernel, once it has waited itself, releases a flag (its first CTA's producer:
+// the wait covers the whole grid before), and the reader acquires it, or waits after all
+// where the flag is not there.  V's kernel clears the flag, and the reader when it ends.
+constexpr uint32_t kReadyFlag = 0x56d2a91eu;
+// A whole warp, after pdl_wait() and before pdl_launch_dependents().
+__device__ __forceinline__ void release_ready(uint32_t* flag) {
+    if (flag && blockIdx.x == 0 && lane_id() == 0) {
+        asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(flag), "r"(kReadyFlag) : "memory");
+        __threadfence();  // performed before the launch that looks for it
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ bool acquire_ready(const uint32_t* flag) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+    return v == kReadyFlag;
 }
 
 // The sum of four floats at the same shared-memory offset in CTAs 0 .. n-1 of the
@@ -315,16 +339,18 @@ int lora_shrink_launch(bool b_mn, const uint16_t* X, const uint16_t* ad, const f
                        int64_t Kred, int r, uint16_t* out, uint16_t* out_lo, uint32_t* zero, int zero_words,
                        int32_t* status, cudaStream_t st);
 // Y = X W^T + U B^T (b_mn false) or dX = dY W + V A (b_mn true): split-reduction
-// clusters for few row tiles, 2-CTA pair tiles otherwise.
+// clusters for few row tiles, 2-CTA pair tiles otherwise.  ready (or null): a cleared word
+// to release once U (V) can be read, for the gradients' kernel.
 int lora_project_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, const uint16_t* ad,
-                        const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, int32_t* status,
-                        cudaStream_t st);
+                        const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, uint32_t* ready,
+                        int32_t* status, cudaStream_t st);
 int lora_pair_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, const uint16_t* ad,
-                     const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, int32_t* status,
-                     cudaStream_t st);
-// dA, dB (either may be null); counters: kGradCtas zeroed words, sums: the CTAs' partial
-// sums, 2 x kGradCtas x 128 x r floats.
+                     const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, uint32_t* ready,
+                     int32_t* status, cudaStream_t st);
+// dA, dB (either may be null); counters: kGradCtas zeroed words, and the flag that dX's
+// kernel releases; sums: the CTAs' partial sums, 2 x kGradCtas x 128 x r floats.
 constexpr int kGradCtas = 320;
+constexpr int kGradWords = kGradCtas + 1;
 // What was launched just before: V's kernel, dX's (itself after V's), or something else.
 enum GradAfter { GRAD_AFTER_V, GRAD_AFTER_DX, GRAD_AFTER_OTHER };
 int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, const uint16_t* V, const uint16_t* V_lo,

@@ -51,7 +51,7 @@ struct GradParams {
     int stage_bytes;
     uint32_t* counter;         // [CTA]: arrivals of the item that CTA began and did not end
     float* sums;               // [CTA][2][r][128]
-    int after_v;               // follows the kernel that writes V and clears the counters
+    uint32_t* ready;           // released by dX's kernel once V and the cleared counters can be read (or null)
     int32_t* status;
 };
 
@@ -64,6 +64,7 @@ struct GradCtl {
     uint32_t tmem_base;
     int abort_flag;
     int last;
+    int ready;              // V can be read: nothing to wait for
     int kind[kGMaxStages];  // of the stage's block: kGathered | kItemEnd | kTwoParts
 };
 
@@ -112,10 +113,6 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
     const int buf_cols = ncols <= 16 ? 16 : (ncols <= 32 ? 32 : (ncols <= 64 ? 64 : (ncols <= 128 ? 128 : 256)));
     constexpr uint32_t piece_bytes = CHUNK * kGK * 2;
 
-    // Launched while the kernel before runs.  That is the one that makes V, to be waited
-    // for, or dX's, which lets this grid start only once V is complete: then nothing here
-    // depends on it, and these CTAs fill the SMs its last tiles leave idle.
-    if (p.after_v) pdl_wait();
     // adapters without tokens get zeros, a piece from every CTA: a lane looks at an
     // adapter, the warp clears those found
     for (int a0 = warp * 32; a0 < p.plan.L; a0 += kGThreads) {
@@ -153,6 +150,7 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
         }
         mbar_init(&ctl->drain, 1);
         ctl->abort_flag = 0;
+        ctl->ready = p.ready && acquire_ready(p.ready);
         fence_barrier_init();
         for (int k = 0; k < 2; ++k)
             if (p.side[k].tiles) tma_prefetch_desc(&maps.wide[k]);
@@ -164,6 +162,11 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // Launched while the kernel before runs.  That is the one that makes V and clears the
+    // counters, to be waited for, or dX's, which makes both visible by its flag: then nothing
+    // here depends on it, and these CTAs fill the SMs its last tiles leave idle.
+    if (ctl->ready) fence_proxy_async();  // V's stores, before this thread's TMA reads of them
+    else pdl_wait();
     const uint32_t tmem = ctl->tmem_base;
     const uint32_t ring0 = smem_u32(ring);
     // Share j ends where share j + 1 begins, at total (j + 1) / G or at an end of the item
@@ -490,6 +493,8 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
     }
 
     pdl_wait();  // this grid does not end before the one before it
+    // (a CTA that starts after this finds no flag and waits, for a grid that has ended)
+    if (p.ready && blockIdx.x == 0 && threadIdx.x == 0) *p.ready = 0;
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -529,13 +534,13 @@ int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, c
                      const PlanView& plan, int64_t K, int64_t N, int r, uint16_t* dA, uint16_t* dB, uint32_t* counters,
                      float* sums, GradAfter after, int32_t* status, cudaStream_t st) {
     GradParams p{};
-    p.after_v = after == GRAD_AFTER_V;
     const bool kernel = after != GRAD_AFTER_OTHER;
     p.plan = plan;
     p.r = r;
     const int chunk = rank_pad(r);
     p.nc = (r + chunk - 1) / chunk;
     p.counter = counters;
+    p.ready = after == GRAD_AFTER_DX ? counters + kGradCtas : nullptr;
     p.sums = sums;
     p.status = status;
     if (dA)

@@ -41,6 +41,7 @@ struct PairParams {
     int cuts;          // pieces of those: 1 or 2
     int64_t items;     // tiles and pieces
     uint16_t* out;
+    uint32_t* ready;   // to release once U (V) can be read (or null)
     int st32;          // output rows start 32-byte aligned
     int32_t* status;
 };
@@ -183,6 +184,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                     if (!waited) {
                         pdl_wait();  // U (V) of the kernel before
                         waited = true;
+                        release_ready(p.ready);
                         pdl_launch_dependents();  // (the next kernel may read it too)
                     }
                     uint8_t* sA = ring + stage * kPStage;
@@ -213,6 +215,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             }
             if (!waited) {
                 pdl_wait();  // the launch before this one has finished before this grid can
+                release_ready(p.ready);
                 pdl_launch_dependents();
             }
             // The even CTA's barriers count both CTAs' copies: let them land.
@@ -397,8 +400,8 @@ int launch_pair(const CUtensorMap (&m)[6], const PairParams& p, int clusters, cu
 }  // namespace
 
 int lora_pair_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, const uint16_t* ad,
-                     const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, int32_t* status,
-                     cudaStream_t st) {
+                     const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, uint32_t* ready,
+                     int32_t* status, cudaStream_t st) {
     PairParams p{};
     p.plan = plan;
     p.Kred = static_cast<int>(Kred);
@@ -418,6 +421,7 @@ int lora_pair_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const uint
     p.whole = tiles - rest;
     p.items = p.whole + rest * p.cuts;
     p.out = out;
+    p.ready = ready;
     p.st32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && ncols % 16 == 0;
     p.status = status;
     CUtensorMap m[6] = {};

@@ -39,6 +39,7 @@ struct ProjectParams {
     int xrows;           // rows of the X boxes (a multiple of 8, at most 128)
     int stages;
     uint16_t* out;
+    uint32_t* ready;     // to release once U (V) can be read (or null)
     int32_t* status;
 };
 
@@ -178,6 +179,7 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 if (!waited) {
                     pdl_wait();  // U (V) of the kernel before
                     waited = true;
+                    release_ready(p.ready);
                     pdl_launch_dependents();  // (the next kernel may read it too)
                 }
                 uint8_t* sA = ring + stage * stage_bytes;
@@ -204,6 +206,7 @@ project_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         }
         if (!waited) {
             pdl_wait();  // the launch before this one has finished before this grid can
+            release_ready(p.ready);
             pdl_launch_dependents();
         }
         // every copy has landed before the ring is reused or the CTA exits
@@ -334,8 +337,8 @@ int launch_project(const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap
 }  // namespace
 
 int lora_project_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, const uint16_t* ad,
-                        const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, int32_t* status,
-                        cudaStream_t st) {
+                        const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, uint32_t* ready,
+                        int32_t* status, cudaStream_t st) {
     ProjectParams p{};
     p.plan = plan;
     p.Kred = static_cast<int>(Kred);
@@ -350,6 +353,7 @@ int lora_project_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const u
     p.stages = kRRing / (p.xrows * 128 + kRSlot);
     if (p.stages > kRMaxStages) p.stages = kRMaxStages;
     p.out = out;
+    p.ready = ready;
     p.status = status;
     CUtensorMap mX{}, mW{}, mU{}, mE{};
     if (!encode_map_2d(&mX, X, Kred, plan.T, Kred, kRK, p.xrows)) return GG_ERR_CUDA;
