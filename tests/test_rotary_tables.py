@@ -1,0 +1,23 @@
+"""Frequency tables at the ends of their arguments' ranges (host only)."""
+import math
+
+import numpy as np
+import pytest
+
+
+@pytest.mark.parametrize("factor", [1.0, 0.5, 1e-3, 1e-6])
+def test_yarn_does_not_scale_down_for_factors_up_to_one(factor):
+    """A context no longer than the trained one: the attention factor stays 1 (0.1 ln(factor) + 1
+    would go below it, and below zero from e^-10 on)."""
+    from unpermute_route_hist_gb300 import rotary
+    inv, m = rotary.frequencies(64, 10000.0, "yarn", factor, original_length=4096)
+    assert m == 1.0
+    base = rotary.frequencies(64, 10000.0)[0]
+    assert np.all(inv >= base * (1 - 1e-12)) and np.all(inv <= base / factor * (1 + 1e-12))
+
+
+def test_yarn_attention_factor_above_one():
+    from unpermute_route_hist_gb300 import rotary
+    for factor in (1.0 + 1e-9, 2.0, 32.0):
+        m = rotary.frequencies(64, 10000.0, "yarn", factor, original_length=4096)[1]
+        assert math.isclose(m, 0.1 * math.log(factor) + 1.0, rel_tol=1e-15)

@@ -8,7 +8,8 @@ Pair i of rot_dim / 2 turns by base^(-2i / rot_dim) radians a position.  Scaling
           factor, the fastest keeps its speed
   yarn    pairs that turn more than beta_fast times over original_length keep their
           speed, those under beta_slow are interpolated by factor, a linear ramp over
-          the pair index between; the result is scaled by 0.1 ln(factor) + 1
+          the pair index between; the result is scaled by 0.1 ln(factor) + 1 (by 1 for
+          a factor up to 1)
 
 The table is computed in 64 bits and held as fractions of a turn in units of 2^-64,
 so the kernel reduces pos * f modulo one turn exactly.
@@ -62,7 +63,7 @@ def frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None,
         low = max(math.floor(pair_of(beta_fast)), 0)
         high = min(math.ceil(pair_of(beta_slow)), rot_dim - 1)
         ramp = np.clip((pairs - low) / max(high - low, 1e-3), 0.0, 1.0)
-        return inv * (1.0 - ramp) + inv / factor * ramp, 0.1 * math.log(factor) + 1.0
+        return inv * (1.0 - ramp) + inv / factor * ramp, 0.1 * math.log(max(factor, 1.0)) + 1.0
     raise ValueError("unknown scaling %r" % (scaling,))
 
 
