@@ -21,3 +21,26 @@ def test_yarn_attention_factor_above_one():
     for factor in (1.0 + 1e-9, 2.0, 32.0):
         m = rotary.frequencies(64, 10000.0, "yarn", factor, original_length=4096)[1]
         assert math.isclose(m, 0.1 * math.log(factor) + 1.0, rel_tol=1e-15)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(base=float("nan")), dict(base=float("inf")), dict(scaling="linear", factor=float("nan")),
+    dict(scaling="linear", factor=float("inf")), dict(scaling="yarn", factor=float("inf"), original_length=4096),
+    dict(scaling="yarn", base=1.0, factor=4.0, original_length=4096),
+    dict(scaling="yarn", base=0.5, factor=4.0, original_length=4096),
+    dict(scaling="yarn", factor=4.0, original_length=-4096),
+    dict(scaling="yarn", factor=4.0, original_length=4096, beta_fast=0.0),
+    dict(scaling="yarn", factor=4.0, original_length=4096, beta_slow=-1.0),
+])
+def test_refuses_what_gives_no_table(bad):
+    """Not finite, or a logarithm of nothing: a ValueError that says so, no table of NaN or zeros."""
+    from unpermute_route_hist_gb300 import rotary
+    with pytest.raises(ValueError, match="must|needs"):
+        rotary.rope_freqs(64, device="cpu", **bad)
+
+
+def test_a_base_below_one_still_gives_a_table():
+    from unpermute_route_hist_gb300 import rotary
+    f = rotary.rope_freqs(8, 0.5, device="cpu")
+    for s, p in zip(f.steps.tolist(), range(4)):
+        assert abs((s % 2 ** 64) / 2.0 ** 64 - (0.5 ** (-p / 4) / (2 * math.pi)) % 1.0) < 2.0 ** -52

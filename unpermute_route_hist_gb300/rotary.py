@@ -43,8 +43,8 @@ def frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None,
     """(radians a position of each pair [rot_dim / 2] float64, attention scale)."""
     if rot_dim < 0 or rot_dim % 2:
         raise ValueError("rot_dim must be even and not negative")
-    if base <= 0 or factor <= 0:
-        raise ValueError("base and factor must be positive")
+    if not (0 < base < math.inf and 0 < factor < math.inf):
+        raise ValueError("base and factor must be positive and finite")
     if scaling == "ntk" and rot_dim > 2:
         base = base * factor ** (rot_dim / (rot_dim - 2))
     pairs = np.arange(rot_dim // 2, dtype=np.float64)
@@ -54,8 +54,10 @@ def frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None,
     if scaling == "linear":
         return inv / factor, 1.0
     if scaling == "yarn":
-        if not original_length:
+        if not original_length or original_length < 0:
             raise ValueError("yarn needs original_length")
+        if base <= 1 or not (beta_fast > 0 and beta_slow > 0):
+            raise ValueError("yarn needs a base above 1 and positive betas")
 
         def pair_of(turns):  # pair index that turns this often over the original length
             return rot_dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
