@@ -454,7 +454,9 @@ int gg_lora_backward(const gg_bf16* dY, const gg_bf16* X, const gg_bf16* W, cons
  *  q, out_q: n_q heads of T tokens, element (t, h, c) at t * tok + h * head + c
  *  (strides in elements, as given per tensor); k, out_k likewise with n_k heads
  *  (n_q or n_k may be 0).  An output may be its input (same strides: in place,
- *  the elements from rot on untouched) or must not overlap it.
+ *  the elements from rot on untouched) or must not overlap it, and its heads must
+ *  not overlap one another (token or head strides below the width written, 0
+ *  included, are refused).
  *  positions [axes, T] int32 (any value); axes > 1: sections (HOST array, axes
  *  entries, sum rot / 2) gives each axis its consecutive pairs, so tokens can
  *  carry a time, a height and a width.

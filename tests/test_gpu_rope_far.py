@@ -31,3 +31,19 @@ def test_strided_heads_past_2_31_elements(gg):
         assert torch.equal(q[-5:], want) and torch.equal(buf[:, H - 1], kept)
     del buf, q, kept
     torch.cuda.empty_cache()
+
+
+def test_one_token_or_one_head_of_any_stride(gg):
+    """A single token's or head's stride does not matter: nothing overlaps."""
+    freqs = gg.rope_freqs(16, device=dev())
+    for T, H in ((1, 4), (5, 1), (1, 1)):
+        x = torch.randn(T, H, 16, dtype=torch.bfloat16, device=dev())
+        pos = torch.arange(1, T + 1, dtype=torch.int32, device=dev())
+        want, _ = gg.rope(x, None, pos, freqs)
+        y = torch.zeros(T, H, 16, dtype=torch.bfloat16, device=dev())
+        out = y.as_strided((T, H, 16), (0 if T == 1 else H * 16, 0 if H == 1 else 16, 1))
+        got, _ = gg.rope(x, None, pos, freqs, out_q=out)
+        assert torch.equal(got, want)
+    x = torch.randn(3, 1, 16, dtype=torch.bfloat16, device=dev()).expand(3, 4, 16)
+    with pytest.raises(gg.GGError):
+        gg.rope(x, None, torch.zeros(3, dtype=torch.int32, device=dev()), freqs, out_q=x)  # four heads in one place

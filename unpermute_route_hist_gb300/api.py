@@ -476,7 +476,7 @@ def rope(q, k, positions, freqs, *, interleaved=False, out_q=None, out_k=None):
     """(q', k'): rotary positions on the heads of q [T, Hq, D] and k [T, Hk, D] (or None), e.g.
     views of a packed projection.  positions [T] int32, or [axes, T] with sections; freqs from
     rope_freqs; interleaved pairs elements (2i, 2i+1), else (i, i + rot/2).  out_q=q, out_k=k
-    turns them in place."""
+    turns them in place; an output's heads may not overlap one another (an expanded tensor is refused)."""
     return _rope(q, k, positions, freqs, interleaved, out_q, out_k, 0)
 
 

@@ -253,6 +253,10 @@ int gg_rope(const void* q, int64_t q_tok, int64_t q_head, int n_q, const void* k
     const bool same = (!n_q || (q == out_q && q_tok == oq_tok && q_head == oq_head)) &&
                       (!n_k || (k == out_k && k_tok == ok_tok && k_head == ok_head));
     if (same && rot == 0) return GG_OK;
+    // an output's heads may not overlap one another: neighbours are as far apart as what is written
+    const int wide = same ? rot : D;
+    auto overlap = [&](int n, int64_t tok, int64_t head) { return (T > 1 && n > 0 && tok < wide) || (n > 1 && head < wide); };
+    if (overlap(n_q, oq_tok, oq_head) || overlap(n_k, ok_tok, ok_head)) return GG_ERR_INVALID_ARG;
     RopeParams p{};
     p.q = RopeHeads{q, out_q, q_tok, q_head, oq_tok, oq_head, n_q};
     p.k = RopeHeads{k, out_k, k_tok, k_head, ok_tok, ok_head, n_k};
