@@ -428,12 +428,15 @@ int gg_lora_forward(const gg_bf16* X, const gg_bf16* W, const gg_bf16* A, const 
 
 /* Gradient of gg_lora_forward (W is frozen; gg_backward_dW gives its gradient):
  *   V[t]  = scale[a] * (dY[t] @ B[a])                     (kept in the workspace)
- *   dX[t] = bf16( dY[t] @ W + V[t] @ A[a] )
+ *   dX[t] = bf16( dY[t] @ W + bf16(V[t]) @ A[a] )         (fp32 accumulate)
  *   dA[a] = bf16( sum over tokens t of adapter a of outer(V[t], X[t]) )
  *   dB[a] = bf16( sum over tokens t of adapter a of outer(dY[t], U[t]) )
  *  dY [T, N], U [T, r] the forward's; dX [T, K], dA [L, r, K], dB [L, N, r] out,
  *  each may be NULL (not computed; its operands may then be NULL too: X for dA,
  *  U for dB, W and A for dX).  An adapter without tokens gets zeros.
+ *  dX takes V rounded to bf16, as the forward takes U (the tensor cores' operand);
+ *  dA, which sums V over tokens, takes it as a bf16 and its remainder as another
+ *  (2^-16 of V).
  *  workspace: gg_lora_backward_workspace_size(T, r) bytes, 16-byte aligned
  *  (whichever gradients are wanted).  Deterministic (fixed reduction orders). */
 size_t gg_lora_backward_workspace_size(int64_t T, int r);
