@@ -435,8 +435,8 @@ int gg_lora_forward(const gg_bf16* X, const gg_bf16* W, const gg_bf16* A, const 
  *  each may be NULL (not computed; its operands may then be NULL too: X for dA,
  *  U for dB, W and A for dX).  An adapter without tokens gets zeros.
  *  dX takes V rounded to bf16, as the forward takes U (the tensor cores' operand);
- *  dA, which sums V over tokens, takes it as a bf16 and its remainder as another
- *  (2^-16 of V).
+ *  dA, which sums V over tokens, takes it as two bf16 of its sign (2^-16 of V), so
+ *  an infinity in X or V stays one.
  *  workspace: gg_lora_backward_workspace_size(T, r) bytes, 16-byte aligned
  *  (whichever gradients are wanted).  Deterministic (fixed reduction orders). */
 size_t gg_lora_backward_workspace_size(int64_t T, int r);

@@ -19,7 +19,7 @@ int check_sizes(int64_t T, int L, int r, int64_t N, int64_t K) {
     return GG_OK;
 }
 
-// The backward's workspace: V, its remainder, the gradients' counters and partial sums.
+// The backward's workspace: V, V in two parts, the gradients' counters and partial sums.
 size_t v_bytes(int64_t T, int r) { return (static_cast<size_t>(T) * r * 2 + 255) / 256 * 256; }
 constexpr size_t kCounterBytes = (kGradWords * sizeof(uint32_t) + 255) / 256 * 256;
 
@@ -79,14 +79,14 @@ int gg_lora_forward(const gg_bf16* X, const gg_bf16* W, const gg_bf16* A, const 
     if (!X || !A || (N > 0 && (!W || !B))) return GG_ERR_INVALID_ARG;
     if (!al16(X) || !al16(W) || !al16(A) || !al16(B)) return GG_ERR_UNSUPPORTED;
     const PlanView v = plan_view(const_cast<void*>(plan), T, L);
-    const int e = lora_shrink_launch(false, X, A, scale, v, K, r, U, nullptr, nullptr, 0, status, st);
+    const int e = lora_shrink_launch(false, X, A, scale, v, K, r, U, nullptr, 0, nullptr, 0, status, st);
     if (e != GG_OK || N == 0) return e;
     return project(false, X, W, U, B, v, K, N, r, Y, nullptr, status, st);
 }
 
 size_t gg_lora_backward_workspace_size(int64_t T, int r) {
     if (T < 0 || r < 1) return 0;
-    return 2 * v_bytes(T, r) + kCounterBytes + static_cast<size_t>(2 * kGradCtas) * 128 * r * sizeof(float);
+    return 3 * v_bytes(T, r) + kCounterBytes + static_cast<size_t>(2 * kGradCtas) * 128 * r * sizeof(float);
 }
 
 int gg_lora_backward(const gg_bf16* dY, const gg_bf16* X, const gg_bf16* W, const gg_bf16* A, const gg_bf16* B,
@@ -113,17 +113,18 @@ int gg_lora_backward(const gg_bf16* dY, const gg_bf16* X, const gg_bf16* W, cons
     const PlanView v = plan_view(const_cast<void*>(plan), T, L);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     uint16_t* V = reinterpret_cast<uint16_t*>(ws);
-    uint16_t* V_lo = reinterpret_cast<uint16_t*>(ws + v_bytes(T, r));
-    uint32_t* counters = reinterpret_cast<uint32_t*>(ws + 2 * v_bytes(T, r));
-    float* sums = reinterpret_cast<float*>(ws + 2 * v_bytes(T, r) + kCounterBytes);
+    const int64_t part = static_cast<int64_t>(v_bytes(T, r) / sizeof(uint16_t));
+    uint16_t* parts = V + part;
+    uint32_t* counters = reinterpret_cast<uint32_t*>(ws + 3 * v_bytes(T, r));
+    float* sums = reinterpret_cast<float*>(ws + 3 * v_bytes(T, r) + kCounterBytes);
     int e;
     if (dX || dA)
-        e = lora_shrink_launch(true, dY, B, scale, v, N, r, V, dA ? V_lo : nullptr, counters, kGradWords, status, st);
+        e = lora_shrink_launch(true, dY, B, scale, v, N, r, V, dA ? parts : nullptr, part, counters, kGradWords, status, st);
     else
         e = cuda_result(cudaMemsetAsync(counters, 0, kGradWords * sizeof(uint32_t), st));
     if (e == GG_OK && dX) e = project(true, dY, W, V, A, v, N, K, r, dX, dA || dB ? counters + kGradCtas : nullptr, status, st);
     if (e == GG_OK && (dA || dB))
-        e = lora_grad_launch(X, dY, U, V, V_lo, v, K, N, r, dA, dB, counters, sums,
+        e = lora_grad_launch(X, dY, U, parts, parts + part, v, K, N, r, dA, dB, counters, sums,
                              dX ? GRAD_AFTER_DX : (dA ? GRAD_AFTER_V : GRAD_AFTER_OTHER), status, st);
     return e;
 }

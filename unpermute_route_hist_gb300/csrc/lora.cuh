@@ -334,10 +334,11 @@ struct ClusterRoom {
 };
 
 // U = scale X A^T (B_MN false; A [L, r, K]) or V = scale dY B (B_MN true; B [L, N, r]).
+// parts (if any): the product as two bf16, the second `part` elements after the first.
 // zero (if any): zero_words 32-bit words that the launch also clears.
 int lora_shrink_launch(bool b_mn, const uint16_t* X, const uint16_t* ad, const float* scale, const PlanView& plan,
-                       int64_t Kred, int r, uint16_t* out, uint16_t* out_lo, uint32_t* zero, int zero_words,
-                       int32_t* status, cudaStream_t st);
+                       int64_t Kred, int r, uint16_t* out, uint16_t* parts, int64_t part, uint32_t* zero,
+                       int zero_words, int32_t* status, cudaStream_t st);
 // Y = X W^T + U B^T (b_mn false) or dX = dY W + V A (b_mn true): split-reduction
 // clusters for few row tiles, 2-CTA pair tiles otherwise.  ready (or null): a cleared word
 // to release once U (V) can be read, for the gradients' kernel.
@@ -347,13 +348,13 @@ int lora_project_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const u
 int lora_pair_launch(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, const uint16_t* ad,
                      const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, uint32_t* ready,
                      int32_t* status, cudaStream_t st);
-// dA, dB (either may be null); counters: kGradCtas zeroed words, and the flag that dX's
+// dA, dB (either may be null) from V's two parts and U; counters: kGradCtas zeroed words, and the flag that dX's
 // kernel releases; sums: the CTAs' partial sums, 2 x kGradCtas x 128 x r floats.
 constexpr int kGradCtas = 320;
 constexpr int kGradWords = kGradCtas + 1;
 // What was launched just before: V's kernel, dX's (itself after V's), or something else.
 enum GradAfter { GRAD_AFTER_V, GRAD_AFTER_DX, GRAD_AFTER_OTHER };
-int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, const uint16_t* V, const uint16_t* V_lo,
+int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, const uint16_t* V_hi, const uint16_t* V_lo,
                      const PlanView& plan, int64_t K, int64_t N, int r, uint16_t* dA, uint16_t* dB, uint32_t* counters,
                      float* sums, GradAfter after, int32_t* status, cudaStream_t st);
 int lora_plan_launch(const int32_t* ids, const PlanView& plan, int32_t* status, cudaStream_t st);

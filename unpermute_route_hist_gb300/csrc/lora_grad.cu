@@ -36,7 +36,7 @@ constexpr int kGMinBlocks = 2;      // of a CTA's share
 
 struct GradSide {
     const uint16_t* wide;      // [T, cols]
-    const uint16_t* narrow[2]; // [T, r]: the operand and its rounding's remainder
+    const uint16_t* narrow[2]; // [T, r]: the operand, in one or two parts
     int parts;                 // 1 or 2 of them
     int cols;
     int tiles;                 // 128-column chunks
@@ -70,11 +70,11 @@ struct GradCtl {
 
 constexpr int kGathered = 1;  // by cp.async
 constexpr int kItemEnd = 2;   // the last of its item here
-constexpr int kTwoParts = 4;  // the narrow operand has a remainder
+constexpr int kTwoParts = 4;  // of the narrow operand
 
 struct GradMaps {
     CUtensorMap wide[2];
-    CUtensorMap narrow[3];     // V, V's remainder, U
+    CUtensorMap narrow[3];     // V's two parts, U
 };
 
 // A CTA's share of the list, walked item by item: adapter a, chunk `tile` of both
@@ -530,7 +530,7 @@ int launch_grad(const GradMaps& m, GradParams p, bool after_kernel, cudaStream_t
 
 }  // namespace
 
-int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, const uint16_t* V, const uint16_t* V_lo,
+int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, const uint16_t* V_hi, const uint16_t* V_lo,
                      const PlanView& plan, int64_t K, int64_t N, int r, uint16_t* dA, uint16_t* dB, uint32_t* counters,
                      float* sums, GradAfter after, int32_t* status, cudaStream_t st) {
     GradParams p{};
@@ -544,14 +544,14 @@ int lora_grad_launch(const uint16_t* X, const uint16_t* dY, const uint16_t* U, c
     p.sums = sums;
     p.status = status;
     if (dA)
-        p.side[0] = GradSide{X, {V, V_lo}, 2, static_cast<int>(K), static_cast<int>((K + kGM - 1) / kGM), dA};
+        p.side[0] = GradSide{X, {V_hi, V_lo}, 2, static_cast<int>(K), static_cast<int>((K + kGM - 1) / kGM), dA};
     if (dB)
         p.side[1] = GradSide{dY, {U, nullptr}, 1, static_cast<int>(N), static_cast<int>((N + kGM - 1) / kGM), dB};
     p.stage_bytes = kGWide + chunk * kGK * 2 * p.nc * (dA ? 2 : 1);
     GradMaps m{};
     if (dA) {
         if (!encode_map_2d(&m.wide[0], X, K, plan.T, K, 64, kGK)) return GG_ERR_CUDA;
-        if (!encode_map_2d(&m.narrow[0], V, r, plan.T, r, chunk, kGK)) return GG_ERR_CUDA;
+        if (!encode_map_2d(&m.narrow[0], V_hi, r, plan.T, r, chunk, kGK)) return GG_ERR_CUDA;
         if (!encode_map_2d(&m.narrow[1], V_lo, r, plan.T, r, chunk, kGK)) return GG_ERR_CUDA;
     }
     if (dB) {

@@ -36,7 +36,8 @@ struct ShrinkParams {
     int stage_bytes, stages;
     const float* scale;
     uint16_t* out;
-    uint16_t* out_lo;  // the rounding's remainder, in bf16 (or null)
+    uint16_t* parts;   // the product as two bf16 (below), [2][T, r] (or null)
+    int64_t part;      // elements from one part to the other
     uint32_t* zero;    // words to clear for the kernels after
     int zero_words;
     int32_t* status;
@@ -50,6 +51,19 @@ struct ShrinkCtl {
     int abort_flag;
     int32_t row[kSM];  // the tile's rows
 };
+
+// v as two bf16 whose sum is v to 2^-16 and which have v's sign, both zero only if v is: the
+// bits above bf16's last, and the rest (2^-24 of v if there is none).  A product with an
+// infinity then is the same infinity for both (a rounded v and its remainder would give
+// inf - inf or inf 0); an infinite or NaN v is both parts.
+__device__ __forceinline__ void two_parts(float v, float& hi, float& lo) {
+    hi = lo = v;
+    if (fabsf(v) < __int_as_float(0x7f800000)) {
+        hi = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+        lo = v - hi;
+        if (lo == 0.f) lo = v * 0x1p-24f;
+    }
+}
 
 constexpr int kShrinkSmem = 1024 + kSRing + 1024;
 static_assert(sizeof(ShrinkCtl) <= 1024, "control block");
@@ -88,7 +102,10 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
                 if (!(bare >> row & 1u)) continue;
                 const int64_t at = (w * 32 + row) * p.r + (lane - sub * per) * 8;
                 *reinterpret_cast<uint4*>(p.out + at) = make_uint4(0, 0, 0, 0);
-                if (p.out_lo) *reinterpret_cast<uint4*>(p.out_lo + at) = make_uint4(0, 0, 0, 0);
+                if (p.parts) {
+                    *reinterpret_cast<uint4*>(p.parts + at) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(p.parts + p.part + at) = make_uint4(0, 0, 0, 0);
+                }
             }
         }
         __syncwarp();
@@ -255,17 +272,17 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ C
             s = make_float4(s.x * sc, s.y * sc, s.z * sc, s.w * sc);
             // U (V) is an operand of the tensor cores: bf16, which moves Y and dX by 0.0006 to
             // 0.0011 of their norm (their own rounding: 0.0017).  The adapter gradients sum V
-            // over tokens: they take its remainder as a second bf16 too
+            // over tokens: they take it as two bf16
             const int64_t at = static_cast<int64_t>(ctl->row[rr]) * p.r + c0 + c;
-            const uint2 hi = pack_bf16x4(s);
-            *reinterpret_cast<uint2*>(p.out + at) = hi;
-            if (p.out_lo) {
-                auto rest = [](float x) {
-                    const float h = __bfloat162float(__float2bfloat16(x));
-                    return fabsf(h) < __int_as_float(0x7f800000) ? x - h : 0.f;
-                };
-                *reinterpret_cast<uint2*>(p.out_lo + at) =
-                    pack_bf16x4(make_float4(rest(s.x), rest(s.y), rest(s.z), rest(s.w)));
+            *reinterpret_cast<uint2*>(p.out + at) = pack_bf16x4(s);
+            if (p.parts) {
+                float4 hi, lo;
+                two_parts(s.x, hi.x, lo.x);
+                two_parts(s.y, hi.y, lo.y);
+                two_parts(s.z, hi.z, lo.z);
+                two_parts(s.w, hi.w, lo.w);
+                *reinterpret_cast<uint2*>(p.parts + at) = pack_bf16x4(hi);
+                *reinterpret_cast<uint2*>(p.parts + p.part + at) = pack_bf16x4(lo);
             }
         }
     }
@@ -302,8 +319,8 @@ int launch_shrink(const CUtensorMap& x, const CUtensorMap& e, const ShrinkParams
 }  // namespace
 
 int lora_shrink_launch(bool b_mn, const uint16_t* X, const uint16_t* ad, const float* scale, const PlanView& plan,
-                       int64_t Kred, int r, uint16_t* out, uint16_t* out_lo, uint32_t* zero, int zero_words,
-                       int32_t* status, cudaStream_t st) {
+                       int64_t Kred, int r, uint16_t* out, uint16_t* parts, int64_t part, uint32_t* zero,
+                       int zero_words, int32_t* status, cudaStream_t st) {
     ShrinkParams p{};
     p.plan = plan;
     p.X = X;
@@ -314,7 +331,8 @@ int lora_shrink_launch(bool b_mn, const uint16_t* X, const uint16_t* ad, const f
     p.chunk = rank_pad(p.take);
     p.scale = scale;
     p.out = out;
-    p.out_lo = out_lo;
+    p.parts = parts;
+    p.part = part;
     p.zero = zero;
     p.zero_words = zero ? zero_words : 0;
     p.status = status;
