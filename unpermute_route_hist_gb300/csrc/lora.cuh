@@ -124,8 +124,7 @@ __device__ __forceinline__ uint32_t idesc_bf16_f32_n(int M, int N, int a_mn_majo
 // The producer and issuer warps run as whole warps: every lane walks the loop and
 // waits, one elected lane issues.  Addresses and descriptors then are the same in every
 // lane, which lets them live in uniform registers; with lane 0 alone on a divergent
-// path the issuer needed 562 cycles for a block of four MMAs whatever their width,
-// 505 (256 columns) and 375 (64 columns) this way.
+// path 8192 rows of 4096 -> 6144 took 256 us, 239 this way, and 777 rows 20 and 18.6.
 __device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0); }
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;

@@ -11,9 +11,11 @@
 // Sorting rows by adapter instead would read and write X and Y once more, or
 // gather X (2.5x slower loads here), and break tiles at every adapter's end.
 //
-// An adapter block costs about a shared one (471 cycles): its adapters' ids and row masks
-// wait in shared memory, copied while the shared blocks run (read from global memory a
-// block ahead they took 977).
+// A shared block costs 517-525 SM cycles and an adapter block of rank 64 523 (one round of 76
+// tiles, by the kernel's cycles at 32, 64 and 128 blocks and at 1 to 33 adapters; the MMAs'
+// own time is 512): an adapter's id and row masks wait in shared memory, copied while the
+// shared blocks run (read from global memory a block ahead: 512 mixed rows of 32 adapters of
+// rank 128 took 63 us instead of 46).
 //
 // 8192 rows of 4096 -> 6144 at rank 32, with the low-rank product before it: 229 us, 1.83
 // PFLOP/s; the tensor pipe is active 88% of this kernel's time.
