@@ -24,12 +24,16 @@ size_t v_bytes(int64_t T, int r) { return (static_cast<size_t>(T) * r * 2 + 255)
 constexpr size_t kCounterBytes = (kGradWords * sizeof(uint32_t) + 255) / 256 * 256;
 
 // Y (or dX) from its operands: tiles with a split reduction, or 2-CTA tiles.  Splitting
-// pays for few rows (whole forwards, split and 2-CTA: 64 rows of 4096 x 4096 18.8 and
-// 20.7 us; 48 of 2048 x 2048, 32 mixed adapters 12.7 and 17.5; it loses at 64 rows of
-// 2048 x 2048 in runs, 13.5 and 12.0), and for a long reduction, the adapters' blocks among
-// it, whose 2-CTA tiles leave half of the GPU idle (300 rows of 4096 x 4096, 4 adapters:
-// 23.5 and 25.9; of 2048 x 2048, 16 mixed adapters of rank 64: 18.2 and 20.7; 512 mixed
-// rows, 32 adapters of rank 128: 33.9 and 45.9; with 4 adapters of few blocks 19 and 16).
+// pays for few rows (whole forwards, split and 2-CTA: 64 rows of 4096 x 4096 15.6 and
+// 19.5 us; 48 of 2048 x 2048, 32 mixed adapters 13.5 and 18.9; 64 in runs 12.4 and 13.0),
+// and for a long reduction, the adapters' blocks among it, whose 2-CTA tiles leave half of
+// the GPU idle.  The two meet near 44 blocks (one adapter, 128 to 513 rows, 8 to 26 tiles: at
+// 40 blocks 14.9-16.4 and 15.0-15.9, at 52 15.5-17.4 and 17.2-18.2; 512 mixed rows of
+// 4096 -> 2048, 32 adapters of rank 128: 33.0 and 44.8, 4 of rank 64: 17.7 and 14.8).
+// Known to be off: 28 to 36 tiles of one adapter (256 rows of 4096 -> 7168: 24.1 and
+// 21.6; 300 rows of 4096 x 4096 22.2 and 20.7, with four adapters 22.5 and 25.4), and many
+// adapters of which few occur, which the host does not know (300 rows of 2048 x 2048, one
+// of 256 adapters of rank 64: 19.2 and 16.8).
 int project(bool b_mn, const uint16_t* X, const uint16_t* W, const uint16_t* U, const uint16_t* ad,
             const PlanView& plan, int64_t Kred, int64_t ncols, int r, uint16_t* out, uint32_t* ready, int32_t* status,
             cudaStream_t st) {
