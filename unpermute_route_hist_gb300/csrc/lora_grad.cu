@@ -150,11 +150,11 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
         }
         mbar_init(&ctl->drain, 1);
         ctl->abort_flag = 0;
-        ctl->ready = p.ready && acquire_ready(p.ready);
         fence_barrier_init();
         for (int k = 0; k < 2; ++k)
             if (p.side[k].tiles) tma_prefetch_desc(&maps.wide[k]);
     }
+    if (threadIdx.x == 64) ctl->ready = p.ready && acquire_ready(p.ready);
     if (warp == 1) {
         tmem_alloc(&ctl->tmem_base, 2 * buf_cols);
         tmem_relinquish();
@@ -165,8 +165,8 @@ grad_kernel(const __grid_constant__ GradMaps maps, const GradParams p) {
     // Launched while the kernel before runs.  That is the one that makes V and clears the
     // counters, to be waited for, or dX's, which makes both visible by its flag: then nothing
     // here depends on it, and these CTAs fill the SMs its last tiles leave idle.
-    if (ctl->ready) fence_proxy_async();  // V's stores, before this thread's TMA reads of them
-    else pdl_wait();
+    if (!ctl->ready) pdl_wait();
+    else if (warp == 0) fence_proxy_async();  // V's stores, before the producer's TMA reads of them
     const uint32_t tmem = ctl->tmem_base;
     const uint32_t ring0 = smem_u32(ring);
     // Share j ends where share j + 1 begins, at total (j + 1) / G or at an end of the item
