@@ -44,3 +44,20 @@ def test_a_base_below_one_still_gives_a_table():
     f = rotary.rope_freqs(8, 0.5, device="cpu")
     for s, p in zip(f.steps.tolist(), range(4)):
         assert abs((s % 2 ** 64) / 2.0 ** 64 - (0.5 ** (-p / 4) / (2 * math.pi)) % 1.0) < 2.0 ** -52
+
+
+def test_a_hand_made_table_is_checked():
+    """The kernel reads rot_dim / 2 steps of 64 bits: a table that holds fewer, or another type, is
+    refused where it is made."""
+    import torch
+    from unpermute_route_hist_gb300.rotary import RopeFreqs
+    steps = torch.arange(4, dtype=torch.int64)
+    assert RopeFreqs(steps, 8, 1.0).axes == 1 and RopeFreqs(steps, 8, 1.0, (1, 3)).axes == 2
+    assert RopeFreqs(steps[:0], 0, 1.0).rot_dim == 0
+    for bad in ((steps[:3], 8), (steps, 6), (steps.to(torch.int32), 8), (steps.double(), 8), (steps.view(2, 2), 8),
+                (torch.arange(8)[::2], 8), (steps, 7), (steps, -8)):
+        with pytest.raises(ValueError):
+            RopeFreqs(*bad, 1.0)
+    for sections in ((1, 2), (-1, 5), ()):
+        with pytest.raises(ValueError):
+            RopeFreqs(steps, 8, 1.0, sections)

@@ -32,6 +32,13 @@ class RopeFreqs:
     sections: tuple | None = None   # pairs of each position axis, or None (one axis)
 
     def __post_init__(self):
+        if self.rot_dim < 0 or self.rot_dim % 2:
+            raise ValueError("rot_dim must be even and not negative")
+        s = self.steps
+        if s.dtype is not torch.int64 or s.shape != (self.rot_dim // 2,) or not s.is_contiguous():
+            raise ValueError("steps must be %d contiguous int64, got %s of %s" % (self.rot_dim // 2, tuple(s.shape), s.dtype))
+        if self.sections is not None and (min(self.sections, default=-1) < 0 or sum(self.sections) != self.rot_dim // 2):
+            raise ValueError("sections must be pair counts that sum to rot_dim / 2")
         # what a call passes on, made once
         axes = 1 if self.sections is None else len(self.sections)
         object.__setattr__(self, "axes", axes)
@@ -76,8 +83,6 @@ def rope_freqs(rot_dim: int, base: float = 10000.0, *, scaling: str | None = Non
     rot_dim / 2), for positions [axes, T]."""
     if sections is not None:
         sections = tuple(int(s) for s in sections)
-        if min(sections, default=-1) < 0 or sum(sections) != rot_dim // 2:
-            raise ValueError("sections must be pair counts that sum to rot_dim / 2")
     inv, m = frequencies(rot_dim, base, scaling, factor, original_length, beta_fast, beta_slow)
     steps = [int(math.ldexp(float(f) / (2 * math.pi), 64)) & (2 ** 64 - 1) for f in inv]
     table = torch.from_numpy(np.array(steps, dtype=np.uint64).view(np.int64).copy())
