@@ -438,7 +438,8 @@ int gg_lora_forward(const gg_bf16* X, const gg_bf16* W, const gg_bf16* A, const 
  *  dA, which sums V over tokens, takes it as two bf16 of its sign (2^-16 of V), so
  *  an infinity in X or V stays one.
  *  workspace: gg_lora_backward_workspace_size(T, r) bytes, 16-byte aligned
- *  (whichever gradients are wanted).  Deterministic (fixed reduction orders). */
+ *  (whichever gradients are wanted; 327680 r bytes of it are partial sums, whatever
+ *  T).  Deterministic (fixed reduction orders). */
 size_t gg_lora_backward_workspace_size(int64_t T, int r);
 int gg_lora_backward(const gg_bf16* dY, const gg_bf16* X, const gg_bf16* W, const gg_bf16* A,
                      const gg_bf16* B, const float* scale, const void* plan, const gg_bf16* U,

@@ -21,7 +21,7 @@
 // block order: nothing waits, and the bits do not depend on who that was.
 //
 // 8192 tokens, 8 adapters of rank 32, 4096 and 6144 columns: 56 us with V's product before it,
-// 4.8 TB/s of X and of dY twice; 14 us after dX, beside whose last tiles it starts.
+// 4.8 TB/s of X and of dY twice; 12 us after dX, beside whose last tiles it starts.
 #include "lora.cuh"
 
 namespace gg {

@@ -17,8 +17,9 @@
 // shared blocks run (read from global memory a block ahead: 512 mixed rows of 32 adapters of
 // rank 128 took 63 us instead of 46).
 //
-// 8192 rows of 4096 -> 6144 at rank 32, with the low-rank product before it: 229 us, 1.83
-// PFLOP/s; the tensor pipe is active 88% of this kernel's time.
+// 8192 rows of 4096 -> 6144 at rank 32, with the low-rank product before it: 231-239 us by box
+// (graph replay), 1.75-1.81 PFLOP/s, 262-270 us a call at the power cap; the tensor pipe is
+// active 88% of this kernel's time.
 //
 // Warp 0: TMA producer; warp 1: tensor memory and, in the even CTA, MMA issue;
 // warps 2-5: epilogue (tensor memory -> bf16 -> 32-byte row pieces).  Every wait

@@ -6,8 +6,9 @@
 // the rank of its bit, no atomic hands out places.
 //
 // Bound by launches: up to 256 rows one CTA does everything in one launch (13 us a
-// call from Python), more take five (22 us at 8192 rows), whose grids of one CTA a
-// unit read the ids once each.
+// call from Python, 3 on the device), more take five (22 us at 8192 rows, 12 on the
+// device).  Each of those needs the one before over all units: the units' entries, each
+// adapter's rows over the units, the adapters' offsets, the rows' places, the tiles.
 #include "lora.cuh"
 
 namespace gg {

@@ -13,9 +13,9 @@
 // by MMAs masked to its rows, rank_pad(r) reduction columns each; a ring stage
 // holds as many adapters as fit.
 //
-// 1 row of 4096 -> 6144 at rank 16, with the low-rank product before it: 15.8 us; W's 50 MB
-// take 8 of them at 6.5 TB/s, the rest is the join and two launches.  48 rows with 32
-// adapters: 20.2 us.
+// 1 row of 4096 -> 6144 at rank 16, with the low-rank product before it: 15.4-16.0 us (graph
+// replay; 18-22 a call); W's 50 MB take 8 of them at 6.5 TB/s, the rest is the join and two
+// launches.  48 rows with 32 adapters: 20.3 us.
 #include "lora.cuh"
 
 namespace gg {
