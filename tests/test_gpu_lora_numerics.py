@@ -77,3 +77,21 @@ def test_an_infinity_in_x_or_dy_stays_one_in_da(gg, T, K, N, r, order):
     want[2, :, 9] = float("nan")
     torch.testing.assert_close(dA, want, rtol=0, atol=0, equal_nan=True)
     torch.testing.assert_close(both, want, rtol=0, atol=0, equal_nan=True)
+
+
+@pytest.mark.parametrize("K,N", [(0, 16), (16, 0), (0, 0)])
+def test_empty_widths(gg, K, N):
+    """No input or no output columns: what has elements is zero, what has none is empty."""
+    T, L, r = 37, 2, 8
+    st = status_tensor()
+    ones = lambda *s: torch.ones(*s, dtype=torch.bfloat16, device=dev())
+    plan = gg.lora_plan(torch.arange(T, dtype=torch.int32, device=dev()) % L, L, status=st)
+    args = (ones(T, K), ones(N, K), ones(L, r, K), ones(L, N, r), None, plan)
+    dirty = lambda *s: torch.full(s, float("nan"), dtype=torch.bfloat16, device=dev())
+    Y, U = gg.lora_forward(*args, out=dirty(T, N), out_u=dirty(T, r), status=st)
+    dX, dA, dB = gg.lora_backward(ones(T, N), *args, U, out=dirty(T, K), out_da=dirty(L, r, K), out_db=dirty(L, N, r),
+                                  status=st)
+    assert status_of(st) == 0
+    assert bool((U == K).all()) and Y.shape == (T, N) and not Y.any()
+    assert dX.shape == (T, K) and dA.shape == (L, r, K) and dB.shape == (L, N, r)
+    assert not dX.any() and not dA.any() and not dB.any()

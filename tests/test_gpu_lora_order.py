@@ -51,3 +51,33 @@ def test_gradients_take_their_own_calls_v(gg, T, K, N, L, r, order, want):
     for i, out in enumerate(got):
         for name, x, y in zip(("dX", "dA", "dB"), out, own[i & 1]):
             assert (x is None and y is None) or torch.equal(x, y), (i, name)
+
+
+def test_two_streams_side_by_side(gg):
+    """Calls on two streams, each with a plan and a workspace of its own, give the bits they give
+    alone."""
+    st = status_tensor()
+    jobs = []
+    for seed, (T, K, N, L, r, order) in ((1, (777, 520, 1032, 5, 64, "mixed")), (2, (200, 2048, 520, 3, 16, "runs"))):
+        g = on_gpu(make(T, K, N, L, r, order, seed=seed))
+        size = gg.lora_backward_workspace_size(T, r)
+
+        def call(g=g, L=L, ws=torch.full((size,), 255, dtype=torch.uint8, device=dev())):
+            plan = gg.lora_plan(g["ids"], L, status=st)
+            args = (g["X"], g["W"], g["A"], g["B"], g["scale"], plan)
+            Y, U = gg.lora_forward(*args, status=st)
+            return (Y, U) + gg.lora_backward(g["dY"], *args, U, workspace=ws, status=st)
+
+        jobs.append((call, call(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[] for _ in jobs]
+    for _ in range(8):
+        for i, (call, _, stream) in enumerate(jobs):
+            with torch.cuda.stream(stream):
+                got[i].append(call())
+    torch.cuda.synchronize()
+    assert status_of(st) == 0
+    for (_, want, _), outs in zip(jobs, got):
+        for out in outs:
+            for name, x, y in zip(("Y", "U", "dX", "dA", "dB"), out, want):
+                assert torch.equal(x, y), name
