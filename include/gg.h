@@ -539,7 +539,8 @@ int gg_swiglu_bwd_act8(const uint8_t* codes, const uint8_t* scales, int fmt, con
  *  w_post, w_pre, gate [K] fp32, token_gate [T] fp32; w_post, gate and token_gate may be
  *  NULL (no norm, 1, 1).
  *  out_x [T, K] bf16, needs w_pre; NULL: no second norm.
- *  Y NULL: the norm of h alone (out_h is not written and may be NULL).
+ *  Y NULL: the norm of h alone (h' is h: res_scale is not used, out_h is not written and
+ *  may be NULL).
  *  out_y [T, K] bf16, or y_codes and y_scales in the 8-bit form fmt (at most one of the
  *  two): y, rounded, for the backward; both may be NULL.
  *  K a multiple of 8, at most GG_NORM_MAX_K; eps > 0 (a row of zeros is normed to zeros).
@@ -566,7 +567,7 @@ int gg_block_norm(const void* h, int h_dtype, const gg_bf16* Y, const int32_t* r
  *  dx [T, K] bf16, NULL without the second norm (w_pre is then NULL too).
  *  h [T, K] of h_dtype: the forward's out_h (without a block: its h).
  *  y [T, K] bf16, or y_codes and y_scales in fmt; none of them: no block (dy, dw_post,
- *  dgate and dtoken_gate NULL).
+ *  dgate and dtoken_gate NULL; dh[t] = G[t], for h' is h).
  *  dy [T, K] bf16; dw_post, dw_pre, dgate [K], dtoken_gate [T] fp32, each may be NULL.
  *  workspace: gg_block_norm_bwd_workspace_size(T, K) bytes, 16-byte aligned: partial sums
  *  over tokens (may be NULL when none of dw_post, dw_pre and dgate is wanted).

@@ -692,7 +692,7 @@ def block_norm(h, y=None, *, w_post=None, w_pre=None, gate=None, token_gate=None
       h'  = res_scale h + gate token_gate norm(y) w_post    (no norm without w_post)
       x   = norm(h') w_pre                                  (None without w_pre)
     norm(v) = v / sqrt(mean(v^2) + eps).  h [T, K] bf16 or fp32, y [T*topk, K] bf16 (None: x is the norm of h, and
-    h' is h); vectors [K] and token_gate [T] fp32; row_id_map and topk_w as unpermute_combine's.  keep: 'bf16',
+    h' is h, whatever res_scale is); vectors [K] and token_gate [T] fp32; row_id_map and topk_w as unpermute_combine's.  keep: 'bf16',
     'int8' or 'e4m3' also gives y_t for block_norm_bwd (a tensor, or an Act8).  out_h=h updates h in place."""
     code = _STREAM_DTYPES.get(h.dtype)
     if code is None:
@@ -735,7 +735,7 @@ def block_norm_bwd(dh, dx, h, y=None, *, w_post=None, w_pre=None, gate=None, tok
                    eps: float = 1e-6, want=(True, True, True), out=None, out_dy=None, workspace=None, status=None):
     """(dh, dy, dw_post, dw_pre, dgate, dtoken_gate): block_norm's gradients from those of its h' (dh [T, K], or
     None) and its x (dx [T, K], None without w_pre), at its h' and its y (a bf16 tensor or an Act8; None: a norm of
-    h alone).  want selects dh, dy and the vectors' gradients (None in the place of the others and of those of
+    h alone, whose h' is h: res_scale is not used).  want selects dh, dy and the vectors' gradients (None in the place of the others and of those of
     absent vectors).  out=dh turns dh in place.  dy goes to unpermute_combine_bwd where expert rows were combined."""
     code = _STREAM_DTYPES.get(h.dtype)
     if code is None:

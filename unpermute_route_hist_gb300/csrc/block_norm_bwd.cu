@@ -395,7 +395,8 @@ int gg_block_norm_bwd(const void* dh, const gg_bf16* dx, const void* h, int h_dt
                             {y_scales, T * act8_scale_pitch(K)}, {w_post, vb}, {gate, vb}, {w_pre, vb}, {token_gate, T * 4}};
         if (outputs_overlap(outs, ins)) return GG_ERR_INVALID_ARG;
     }
-    NormBwd p{dh, dx, h, y, y_codes, y_scales, w_post, gate, token_gate, w_pre, res_scale, eps, T,
+    // without a block h' is h: the scale is the residual's beside one
+    NormBwd p{dh, dx, h, y, y_codes, y_scales, w_post, gate, token_gate, w_pre, has_y ? res_scale : 1.f, eps, T,
               static_cast<int>(K), static_cast<int>(norm_half(K)), out_dh, dy, dtoken_gate, sums ? static_cast<float*>(workspace) : nullptr, status,
               0, 0, K % 16 == 0 && aligned(out_dh, 32) && aligned(dy, 32)};
     const int k = p.K, part = p.half;
