@@ -546,8 +546,9 @@ int gg_swiglu_bwd_act8(const uint8_t* codes, const uint8_t* scales, int fmt, con
  *  K a multiple of 8, at most GG_NORM_MAX_K; eps > 0 (a row of zeros is normed to zeros).
  *  Squares are summed in fp32: a row whose sum of squares passes its range is normed to
  *  zeros.  Rows are copied behind bounded waits (status: GG_DEV_TIMEOUT).
- *  Other outputs may not overlap inputs or one another (GG_ERR_INVALID_ARG).  No
- *  counterpart on the pages. */
+ *  Outputs may not overlap inputs or one another (GG_ERR_INVALID_ARG), but out_h may be h:
+ *  the whole of it, and then no other input's memory, but for a Y of the same address and
+ *  bf16 rows with topk = 1 and no map.  No counterpart on the pages. */
 int gg_block_norm(const void* h, int h_dtype, const gg_bf16* Y, const int32_t* row_id_map,
                   const float* topk_w, int topk, const float* w_post, const float* gate,
                   const float* token_gate, float res_scale, const float* w_pre, float eps,
@@ -571,7 +572,9 @@ int gg_block_norm(const void* h, int h_dtype, const gg_bf16* Y, const int32_t* r
  *  dy [T, K] bf16; dw_post, dw_pre, dgate [K], dtoken_gate [T] fp32, each may be NULL.
  *  workspace: gg_block_norm_bwd_workspace_size(T, K) bytes, 16-byte aligned: partial sums
  *  over tokens (may be NULL when none of dw_post, dw_pre and dgate is wanted).
- *  Outputs (but out_dh) overlap neither inputs nor one another, the workspace among them.
+ *  Outputs, the workspace among them, overlap neither inputs nor one another
+ *  (GG_ERR_INVALID_ARG), but out_dh may be dh: the whole of it, and then no other input's
+ *  memory, but for dx, h or y of the same address and as long rows.
  *  Deterministic (fixed summation orders). */
 size_t gg_block_norm_bwd_workspace_size(int64_t T, int64_t K);
 int gg_block_norm_bwd(const void* dh, const gg_bf16* dx, const void* h, int h_dtype,

@@ -82,18 +82,24 @@ inline bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return a && b && an > 0 && bn > 0 && x < y + static_cast<uint64_t>(bn) && y < x + static_cast<uint64_t>(an);
 }
+// A tensor of a call; `row`: the bytes of a row where row t is read or written for token t
+// alone, 0 for all others.
 struct Span {
     const void* at;
     int64_t bytes;
+    int64_t row = 0;
 };
-// Whether an output shares a byte with an input or with another output.
+// Whether an output shares a byte with an input or with another output.  An output of rows may
+// be an input of rows as long (each is read before it is written, by the CTA that writes it).
 template <int N, int M>
 inline bool outputs_overlap(const Span (&out)[N], const Span (&in)[M]) {
     for (int i = 0; i < N; ++i) {
         for (int j = 0; j < i; ++j)
             if (overlap(out[i].at, out[i].bytes, out[j].at, out[j].bytes)) return true;
-        for (int j = 0; j < M; ++j)
+        for (int j = 0; j < M; ++j) {
+            if (out[i].row && out[i].at == in[j].at && out[i].row == in[j].row) continue;
             if (overlap(out[i].at, out[i].bytes, in[j].at, in[j].bytes)) return true;
+        }
     }
     return false;
 }

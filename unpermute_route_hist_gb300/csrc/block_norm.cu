@@ -360,9 +360,10 @@ extern "C" int gg_block_norm(const void* h, int h_dtype, const gg_bf16* Y, const
     const bool f32 = h_dtype == GG_DTYPE_F32;
     const int64_t hb = T * K * (f32 ? 4 : 2), xb = T * K * 2, pitch = act8_code_pitch(K), spitch = act8_scale_pitch(K);
     {
-        // out_h may be h itself: a row is read before it is written, by the CTA that does
-        const Span outs[] = {{out_x, xb}, {out_y, xb}, {y_codes, T * pitch}, {y_scales, T * spitch}, {out_h == h ? nullptr : out_h, hb}};
-        const Span ins[] = {{h, hb}, {Y, xb * topk}, {w_post, K * 4}, {gate, K * 4}, {w_pre, K * 4}, {token_gate, T * 4},
+        // out_h may be h itself; Y may then be h too, where its rows are the tokens'
+        const int64_t row = hb / T, y_row = topk == 1 && !row_id_map ? 2 * K : 0;
+        const Span outs[] = {{out_x, xb}, {out_y, xb}, {y_codes, T * pitch}, {y_scales, T * spitch}, {Y ? out_h : nullptr, hb, out_h == h ? row : 0}};
+        const Span ins[] = {{h, hb, row}, {Y, xb * topk, y_row}, {w_post, K * 4}, {gate, K * 4}, {w_pre, K * 4}, {token_gate, T * 4},
                             {row_id_map, T * topk * 4}, {topk_w, T * topk * 4}};
         if (outputs_overlap(outs, ins)) return GG_ERR_INVALID_ARG;
     }

@@ -387,11 +387,12 @@ int gg_block_norm_bwd(const void* dh, const gg_bf16* dx, const void* h, int h_dt
     const bool f32 = h_dtype == GG_DTYPE_F32;
     {
         const int64_t hb = T * K * (f32 ? 4 : 2), xb = T * K * 2, vb = K * 4;
-        // out_dh may be dh itself: a row is read before it is written, by the CTA that does
+        // out_dh may be dh itself; the other rows may then be dh too
+        const int64_t row = hb / T;
         const Span outs[] = {{dy, xb}, {dw_post, vb}, {dw_pre, vb}, {dgate, vb}, {dtoken_gate, T * 4},
                              {sums ? workspace : nullptr, static_cast<int64_t>(gg_block_norm_bwd_workspace_size(T, K))},
-                             {out_dh == dh ? nullptr : out_dh, hb}};
-        const Span ins[] = {{dh, hb}, {dx, xb}, {h, hb}, {y, xb}, {y_codes, T * act8_code_pitch(K)},
+                             {out_dh, hb, out_dh == dh ? row : 0}};
+        const Span ins[] = {{dh, hb, row}, {dx, xb, 2 * K}, {h, hb, row}, {y, xb, 2 * K}, {y_codes, T * act8_code_pitch(K)},
                             {y_scales, T * act8_scale_pitch(K)}, {w_post, vb}, {gate, vb}, {w_pre, vb}, {token_gate, T * 4}};
         if (outputs_overlap(outs, ins)) return GG_ERR_INVALID_ARG;
     }
