@@ -511,7 +511,8 @@ int gg_act8_unpack(const uint8_t* codes, const uint8_t* scales, int fmt, int64_t
  * fp32 accumulators to codes [R, 32 ceil(N / 32)] and scales in the epilogue (it is
  * never stored in bf16); A [R, N/2] as there, from the fp32 y (its quotient is within two
  * fp32 steps, and 0 for gates under -87.3, where silu is under 2^-119).  The other
- * arguments as there. */
+ * arguments as there.  Codes, scales and A overlap neither inputs (m_sizes and gather_idx
+ * among them) nor one another (GG_ERR_INVALID_ARG). */
 int gg_forward_swiglu_act8(const gg_bf16* X, const gg_bf16* W, const int32_t* m_sizes,
                            const int32_t* gather_idx, int64_t T, int topk, int E, int64_t N,
                            int64_t K, int permute_x, int fmt, uint8_t* codes, uint8_t* scales,

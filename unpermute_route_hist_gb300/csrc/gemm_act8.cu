@@ -56,7 +56,7 @@ extern "C" int gg_forward_swiglu_act8(const gg_bf16* X, const gg_bf16* W, const 
     if (K > 0 && (!al16(X) || !al16(W))) return GG_ERR_UNSUPPORTED;
     if (K > 0 && (N > INT64_MAX / 2 / E / K || R > INT64_MAX / 2 / K)) return GG_ERR_UNSUPPORTED;
     const Span outs[] = {{codes, R * act8_code_pitch(N)}, {scales, R * act8_scale_pitch(N)}, {A, R * N}};
-    const Span ins[] = {{X, (permute_x ? T : R) * K * 2}, {W, E * N * K * 2}};
+    const Span ins[] = {{X, (permute_x ? T : R) * K * 2}, {W, E * N * K * 2}, {m_sizes, int64_t(E) * 4}, {gather_idx, R * 4}};
     if (outputs_overlap(outs, ins)) return GG_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (K == 0) {  // y = 0: codes of 0 under the least scale
