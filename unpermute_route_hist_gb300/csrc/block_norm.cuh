@@ -329,9 +329,11 @@ __device__ __forceinline__ void cta_sum(float (&v)[N], Ctl* ctl, int turn) {
 
 
 // The barrier's phase, with a limit.  A wait that runs out raises the CTA's flag, which
-// every thread reads behind the next barrier: the CTA leaves as one.
-__device__ __forceinline__ void wait_row(uint64_t* bar, uint32_t parity, Ctl* ctl, int32_t* status) {
-    (void)mbar_wait(bar, parity, &ctl->abort_flag, status);
+// every thread reads behind the next barrier: the CTA leaves as one, and until it does
+// nothing more is copied (the stage's phase is not over: a second fill would arrive on it).
+__device__ __forceinline__ void wait_row(uint64_t* bar, uint32_t parity, Ctl* ctl, int32_t* status,
+                                         uint64_t limit_ns = kWaitLimitNs) {
+    (void)mbar_wait(bar, parity, &ctl->abort_flag, status, 0, limit_ns);
 }
 __device__ __forceinline__ bool given_up(const Ctl* ctl) {
     return *reinterpret_cast<const volatile int*>(&ctl->abort_flag) != 0;
@@ -340,8 +342,10 @@ __device__ __forceinline__ bool given_up(const Ctl* ctl) {
 // Row sums: over the CTA, or with SPLIT over the two CTAs of a cluster that have a row's
 // halves (at most seven).  Each sends its sums to the other's shared memory, where they
 // complete on a barrier (`call` counts the calls: two buffers in turn, each used again only
-// behind the other's next sums).  Both add the same two numbers, so they hold the same bits,
-// and both learn whether either gave up: they leave their loops with the same row.  (A barrier of
+// behind the other's next sums).  Both add the same two numbers, so they hold the same bits.
+// True: the caller drains its ring and leaves.  With the sums a CTA says whether it had given
+// up, so the other leaves with the same row; one whose wait for the sums themselves runs out
+// has sent its own already, and the other leaves when the next do not come.  (A barrier of
 // the cluster in its place waits for the stores of the row before: 2048 x 16384 76 us forward
 // and 90 backward from int8.)
 template <int N, bool SPLIT>
@@ -372,16 +376,54 @@ __device__ __forceinline__ bool row_sum(float (&v)[N], Ctl* ctl, uint32_t& call,
     return left;
 }
 
-// Behind a wait that ran out: the copies issued so far land (or their waits run out as
-// well) before the CTA leaves its shared memory.  The thread that issued them.  (Not inline:
-// its registers would spill others of the loops in front of it.)
-__device__ __noinline__ void drain_ring(Ctl* ctl, int stages, int64_t issued) {
+// Behind a wait that ran out, here or in the CTA that has the rows' other halves: the copies
+// issued so far land (or their waits run out as well) before the CTA leaves its shared memory.
+// The thread that issued them.  (Not inline: its registers would spill others of the loops in
+// front of it.)
+__device__ __noinline__ void drain_ring(Ctl* ctl, int stages, int64_t issued, uint64_t limit_ns = kWaitLimitNs) {
     for (int s = 0; s < stages; ++s) {
         const int64_t n = issued / stages + (s < issued % stages ? 1 : 0);
         int dummy = 0;
-        if (n > 0) (void)mbar_wait(&ctl->full[s], static_cast<uint32_t>(n - 1) & 1u, &dummy, nullptr);
+        if (n > 0) (void)mbar_wait(&ctl->full[s], static_cast<uint32_t>(n - 1) & 1u, &dummy, nullptr, 0, limit_ns);
     }
 }
+
+// The diagnostic form of the kernels (gg_selftest_block_norm_wait, _bwd_wait): of one token's
+// rows (their first stage, the first half) the copies are left out, so that the wait for them
+// runs out, and each CTA records how it left.
+constexpr uint64_t kProbeWaitNs = 20000000ull;  // for rows; 2 s still for the other CTA's sums
+struct Probe {
+    int64_t withheld = -1;
+    int32_t* record = nullptr;  // [CTAs][3]: left early; stages filled and not waited for; fills of unfinished phases
+};
+// Thread 0's account of a CTA's ring.
+template <bool ON>
+struct Account {
+    __device__ __forceinline__ void fill(Ctl*, int, int64_t) {}
+    __device__ __forceinline__ void waited() {}
+    __device__ __forceinline__ void drained() {}
+    __device__ __forceinline__ void put(const Probe&, bool, int64_t) const {}
+};
+template <>
+struct Account<true> {
+    int64_t waits = 0;
+    int bad = 0;
+    bool drain = false;
+    // the n-th fill of the ring is about to be issued
+    __device__ __forceinline__ void fill(Ctl* ctl, int stages, int64_t n) {
+        if (threadIdx.x == 0 && n >= stages)
+            bad += mbar_try_wait(&ctl->full[n % stages], static_cast<uint32_t>(n / stages - 1) & 1u) ? 0 : 1;
+    }
+    __device__ __forceinline__ void waited() { ++waits; }
+    __device__ __forceinline__ void drained() { drain = true; }
+    __device__ __forceinline__ void put(const Probe& p, bool left, int64_t fills) const {
+        if (threadIdx.x != 0) return;
+        int32_t* r = p.record + 3 * static_cast<int64_t>(blockIdx.x);
+        r[0] = left;
+        r[1] = drain ? 0 : static_cast<int32_t>(fills - waits);
+        r[2] = bad;
+    }
+};
 
 // `sums`: the sums of a row that a cluster's two CTAs send each other, 0 where a CTA has whole rows.
 __device__ __forceinline__ void init_ring(Ctl* ctl, int stages, uint32_t arrivals, int sums) {

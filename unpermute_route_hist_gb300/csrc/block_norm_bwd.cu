@@ -30,6 +30,7 @@ struct NormBwd {
     int h_bytes, dh_bytes, dx_bytes, y_bytes, sc_bytes;
     int dh_at, dx_at, y_at, sc_at, tg_at;
     float inv_k;
+    Probe probe;
 };
 
 enum KeptY { Y_NONE = 0, Y_BF16 = 1, Y_INT8 = 2, Y_E4M3 = 3 };
@@ -44,7 +45,7 @@ enum KeptY { Y_NONE = 0, Y_BF16 = 1, Y_INT8 = 2, Y_E4M3 = 3 };
 // without.  (Units of 8 columns and twice the threads, 64 registers each: 91 us, for a row's
 // sums and factors are every thread's.)
 // SPLIT: a cluster's two CTAs have halves of each row.
-template <bool F32, int YK, bool SPLIT, bool FULL, bool ALL>
+template <bool F32, int YK, bool SPLIT, bool FULL, bool ALL, bool PROBE = false>
 __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_bwd_kernel(const NormBwd p) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int hs = F32 ? 4 : 2;
@@ -81,15 +82,19 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_bwd_kernel(const No
 
     int64_t t_in = first;
     int s_in = 0;
+    Account<PROBE> account;
+    constexpr uint64_t limit = PROBE ? kProbeWaitNs : kWaitLimitNs;
     // Warp 0 loads: lane 0 the rows, all of them the scales and the gate in words (rows of
     // scales have no 16-byte alignment), whose arrivals the barrier counts as they land.
     auto refill = [&]() {
         if (warp_id() != 0 || t_in >= p.T) return;
         uint8_t* to = ring + s_in * p.stage_bytes;
         uint64_t* bar = &ctl->full[s_in];
+        if constexpr (PROBE) account.fill(ctl, p.stages, (t_in - first) / step);
+        const bool held = PROBE && t_in == p.probe.withheld && side == 0;
         if (lane_id() == 0) {
             mbar_arrive_expect_tx(bar, h_copied + dh_copied + dx_copied + y_copied);
-            if (h_copied) bulk_row(to, from_h + t_in * p.h_bytes, h_copied, bar);
+            if (h_copied && !held) bulk_row(to, from_h + t_in * p.h_bytes, h_copied, bar);
             if (dh_copied) bulk_row(to + p.dh_at, from_dh + t_in * p.dh_bytes, dh_copied, bar);
             if (dx_copied) bulk_row(to + p.dx_at, from_dx + t_in * p.dx_bytes, dx_copied, bar);
             if (YK != Y_NONE) bulk_row(to + p.y_at, from_y + t_in * p.y_bytes, y_copied, bar);
@@ -118,10 +123,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_bwd_kernel(const No
     constexpr int SC = F32 ? 4 : 1;
     int stage = 0;
     uint32_t parity = 0, calls = 0;
-    bool at_first = true;
+    bool at_first = true, left = false;
     for (int64_t t = first; t < p.T; t += step) {
         const uint8_t* rows = ring + stage * p.stage_bytes;
-        wait_row(&ctl->full[stage], parity, ctl, p.status);
+        wait_row(&ctl->full[stage], parity, ctl, p.status, limit);
+        account.waited();
         const float tg = p.token_gate ? *reinterpret_cast<const float*>(rows + p.tg_at) : 1.f;
         auto scale = [&](int j) { return cols.holds(j) ? rows[p.sc_at + (cols.column(j) >> 5)] : uint8_t(0); };
         const float factor = YK >= Y_INT8 && !F32 ? act8_factor(scale(0)) : 1.f;
@@ -190,7 +196,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_bwd_kernel(const No
 #pragma unroll
             for (int k = 3; k < 6; ++k) sum[k] += factor * both(s[k]);
         }
-        bool left;
         if (YK == Y_NONE) {
             float two[2] = {sum[0], sum[1]};
             left = row_sum<2, SPLIT>(two, ctl, calls, p.status);
@@ -261,7 +266,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_bwd_kernel(const No
         }
     }
     asm volatile("griddepcontrol.launch_dependents;");
-    if (threadIdx.x == 0 && given_up(ctl)) drain_ring(ctl, p.stages, (t_in - first) / step);
+    // (left: a CTA whose own waits all ended leaves as well when the other half's gave up)
+    if (left && threadIdx.x == 0) {
+        drain_ring(ctl, p.stages, (t_in - first) / step, limit);
+        account.drained();
+    }
+    account.put(p.probe, left, (t_in - first) / step);
     if (p.part) {
         float* to = p.part + first * 2 * p.K + col0;
         cols.put_sums(to, pre);
@@ -336,24 +346,23 @@ int launch_bwd(const NormBwd& p, const Launch& l) {
            : l.all ? launch_bwd<F32, YK, false, false, true>(p, l)
                    : launch_bwd<F32, YK, false, false, false>(p, l);
 }
+// The diagnostic form: a bf16 stream and y.
+template <bool SPLIT>
+int launch_probe(const NormBwd& p, const Launch& l) {
+    static std::atomic<uint64_t> done;
+    return launch(block_norm_bwd_kernel<false, Y_BF16, SPLIT, false, true, true>, done, p, SPLIT, l.rows, l.threads, l.smem, l.st);
+}
 
-}  // namespace
-}  // namespace gg
-
-using namespace gg;
-
-extern "C" {
-
-size_t gg_block_norm_bwd_workspace_size(int64_t T, int64_t K) {
+size_t workspace_size(int64_t T, int64_t K) {
     if (T <= 0 || K <= 0 || K > GG_NORM_MAX_K) return 0;
     return static_cast<size_t>(bwd_parts(T, K)) * 2 * static_cast<size_t>(K) * sizeof(float);
 }
 
-int gg_block_norm_bwd(const void* dh, const gg_bf16* dx, const void* h, int h_dtype, const gg_bf16* y,
-                      const uint8_t* y_codes, const uint8_t* y_scales, int fmt, const float* w_post,
-                      const float* gate, const float* token_gate, float res_scale, const float* w_pre, float eps,
-                      int64_t T, int64_t K, void* out_dh, gg_bf16* dy, float* dw_post, float* dw_pre, float* dgate,
-                      float* dtoken_gate, void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+int block_norm_bwd(const void* dh, const gg_bf16* dx, const void* h, int h_dtype, const gg_bf16* y, const uint8_t* y_codes,
+                   const uint8_t* y_scales, int fmt, const float* w_post, const float* gate, const float* token_gate,
+                   float res_scale, const float* w_pre, float eps, int64_t T, int64_t K, void* out_dh, gg_bf16* dy,
+                   float* dw_post, float* dw_pre, float* dgate, float* dtoken_gate, void* workspace,
+                   size_t workspace_bytes, int32_t* status, void* stream, const Probe* probe) {
     if (T < 0 || K < 0) return GG_ERR_INVALID_ARG;
     if (h_dtype != GG_DTYPE_BF16 && h_dtype != GG_DTYPE_F32) return GG_ERR_INVALID_ARG;
     if (fmt != GG_ACT8_INT8 && fmt != GG_ACT8_E4M3) return GG_ERR_INVALID_ARG;
@@ -383,14 +392,14 @@ int gg_block_norm_bwd(const void* dh, const gg_bf16* dx, const void* h, int h_dt
             }
         return dtoken_gate && T > 0 ? cuda_result(cudaMemsetAsync(dtoken_gate, 0, static_cast<size_t>(T) * 4, st)) : GG_OK;
     }
-    if (sums && (!workspace || workspace_bytes < gg_block_norm_bwd_workspace_size(T, K))) return GG_ERR_WORKSPACE;
+    if (sums && (!workspace || workspace_bytes < workspace_size(T, K))) return GG_ERR_WORKSPACE;
     const bool f32 = h_dtype == GG_DTYPE_F32;
     {
         const int64_t hb = T * K * (f32 ? 4 : 2), xb = T * K * 2, vb = K * 4;
         // out_dh may be dh itself; the other rows may then be dh too
         const int64_t row = hb / T;
         const Span outs[] = {{dy, xb}, {dw_post, vb}, {dw_pre, vb}, {dgate, vb}, {dtoken_gate, T * 4},
-                             {sums ? workspace : nullptr, static_cast<int64_t>(gg_block_norm_bwd_workspace_size(T, K))},
+                             {sums ? workspace : nullptr, static_cast<int64_t>(workspace_size(T, K))},
                              {out_dh, hb, out_dh == dh ? row : 0}};
         const Span ins[] = {{dh, hb, row}, {dx, xb, 2 * K}, {h, hb, row}, {y, xb, 2 * K}, {y_codes, T * act8_code_pitch(K)},
                             {y_scales, T * act8_scale_pitch(K)}, {w_post, vb}, {gate, vb}, {w_pre, vb}, {token_gate, T * 4}};
@@ -437,6 +446,10 @@ int gg_block_norm_bwd(const void* dh, const gg_bf16* dx, const void* h, int h_dt
     const bool all = dh && dx && out_dh && (dy || !has_y);
     const Launch l{norm_split(K), all && p.st32 && K == 16 * threads, all, static_cast<unsigned>(T < most ? T : most), threads,
                    sizeof(Ctl) + static_cast<size_t>(p.stages) * p.stage_bytes, st};
+    if (probe) {
+        p.probe = *probe;
+        return l.split ? launch_probe<true>(p, l) : launch_probe<false>(p, l);
+    }
     const int kind = y ? Y_BF16 : !y_codes ? Y_NONE : fmt == GG_ACT8_INT8 ? Y_INT8 : Y_E4M3;
 #define GG_BWD(F)                                        \
     (kind == Y_NONE   ? launch_bwd<F, Y_NONE>(p, l)      \
@@ -457,6 +470,36 @@ int gg_block_norm_bwd(const void* dh, const gg_bf16* dx, const void* h, int h_dt
     cfg.numAttrs = 1;
     return cuda_result(cudaLaunchKernelEx(&cfg, block_norm_sum_kernel, static_cast<const float*>(p.part),
                                           static_cast<int>(l.rows), p.K, w_post, gate, dw_post, dw_pre, dgate));
+}
+
+}  // namespace
+}  // namespace gg
+
+using namespace gg;
+
+extern "C" {
+
+size_t gg_block_norm_bwd_workspace_size(int64_t T, int64_t K) { return workspace_size(T, K); }
+
+int gg_block_norm_bwd(const void* dh, const gg_bf16* dx, const void* h, int h_dtype, const gg_bf16* y,
+                      const uint8_t* y_codes, const uint8_t* y_scales, int fmt, const float* w_post,
+                      const float* gate, const float* token_gate, float res_scale, const float* w_pre, float eps,
+                      int64_t T, int64_t K, void* out_dh, gg_bf16* dy, float* dw_post, float* dw_pre, float* dgate,
+                      float* dtoken_gate, void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+    return block_norm_bwd(dh, dx, h, h_dtype, y, y_codes, y_scales, fmt, w_post, gate, token_gate, res_scale, w_pre, eps, T,
+                          K, out_dh, dy, dw_post, dw_pre, dgate, dtoken_gate, workspace, workspace_bytes, status, stream,
+                          nullptr);
+}
+
+int gg_selftest_block_norm_bwd_wait(const gg_bf16* dx, const gg_bf16* h, const gg_bf16* y, const float* w, int64_t T,
+                                    int64_t K, int64_t withheld, gg_bf16* out_dh, gg_bf16* dy, int32_t* record,
+                                    int32_t* status, void* stream) {
+    if (!dx || !y || !w || !out_dh || !dy || !record || !status || withheld < 0 || withheld >= T) return GG_ERR_INVALID_ARG;
+    Probe probe;
+    probe.withheld = withheld;
+    probe.record = record;
+    return block_norm_bwd(dx, dx, h, GG_DTYPE_BF16, y, nullptr, nullptr, GG_ACT8_INT8, w, nullptr, nullptr, 1.f, w, 1e-6f, T,
+                          K, out_dh, dy, nullptr, nullptr, nullptr, nullptr, nullptr, 0, status, stream, &probe);
 }
 
 }  // extern "C"
