@@ -150,15 +150,19 @@ int gg_set_gemm_schedule(int mode);
  * a hang, leaving the context usable.  No counterpart on the pages. */
 int gg_selftest_bounded_wait(int32_t* status, int32_t* result, uint64_t limit_ns, void* stream);
 
-/* Diagnostic: gg_block_norm_bwd (bf16 stream and y, dh = dx, w_post = w_pre = w, eps 1e-6, no
- * vectors' gradients), except that of token `withheld` (< T) one copy is left out (of a row
- * that two CTAs share, the first half's): the wait for it runs out after 20 ms, the CTAs
- * that have the row leave early and status is GG_DEV_TIMEOUT.
+/* Diagnostic: gg_block_norm (bf16 stream, topk > 3 rows a token in token-slot order with
+ * weights 1, w_post = w_pre = w, eps 1e-6) and gg_block_norm_bwd (bf16 stream and y, dh = dx,
+ * the same w, no vectors' gradients), except that of token `withheld` (< T) the copies of one
+ * stage are left out (of a row that two CTAs share, the first half's): the wait for them runs
+ * out after 20 ms, the CTAs that have the row leave early and status is GG_DEV_TIMEOUT.
  *  record [CTAs, 3] int32, CTAs <= 2432, those behind the launch's left as they were: whether a
  *  CTA left early; stages that it filled and left without waiting for them (0, or its shared
  *  memory would be written behind it); stages that it filled again before they were full (0).
  * Tokens of other CTAs come out as they would; those of the CTAs that left are as they
  * were from the withheld one on.  No counterpart on the pages. */
+int gg_selftest_block_norm_wait(const gg_bf16* h, const gg_bf16* Y, int topk, const float* w, int64_t T,
+                                int64_t K, int64_t withheld, gg_bf16* out_h, gg_bf16* out_x,
+                                int32_t* record, int32_t* status, void* stream);
 int gg_selftest_block_norm_bwd_wait(const gg_bf16* dx, const gg_bf16* h, const gg_bf16* y, const float* w,
                                     int64_t T, int64_t K, int64_t withheld, gg_bf16* out_dh, gg_bf16* dy,
                                     int32_t* record, int32_t* status, void* stream);

@@ -61,6 +61,27 @@ def test_backward(lib, T, K, groups):
     assert all(torch.equal(a, b) for a, b in zip(call(), want))
 
 
+# several stages a token: 64 rows of 4104 columns (152 CTAs), 40 of 8456 (76 clusters)
+@pytest.mark.parametrize("T,K,topk,groups", [(152 * 3 + 5, 4104, 64, 152), (76 * 3 + 5, 8456, 40, 76)])
+def test_forward(lib, T, K, topk, groups):
+    h, Y = rows(T, K, 1), rows(T * topk, K, 2)
+    w = torch.rand(K, device=dev()) + 0.5
+    call = lambda: gg.block_norm(h, Y, w_post=w, w_pre=w, topk=topk)[:2]
+    want = call()
+    for turn in (0, 1):
+        withheld = turn * groups + 10
+        outs = [torch.full_like(h, KEPT) for _ in range(2)]
+        record = torch.full((3 * 2432,), UNUSED, dtype=torch.int32, device=dev())
+        status = status_tensor()
+        rc = lib.gg_selftest_block_norm_wait(h.data_ptr(), Y.data_ptr(), topk, w.data_ptr(), T, K, withheld, outs[0].data_ptr(),
+                                             outs[1].data_ptr(), record.data_ptr(), status.data_ptr(),
+                                             torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        check(record, status, groups, K > 8192, T, withheld, outs, want)
+    assert all(torch.equal(a, b) for a, b in zip(call(), want))
+
+
 def test_refusals(lib):
     assert lib.gg_selftest_block_norm_bwd_wait(None, None, None, None, 4, 64, 0, None, None, None, None, None) == \
         _lib.GG_ERR_INVALID_ARG
+    assert lib.gg_selftest_block_norm_wait(None, None, 8, None, 4, 64, 0, None, None, None, None, None) == _lib.GG_ERR_INVALID_ARG

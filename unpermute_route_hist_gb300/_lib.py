@@ -28,6 +28,7 @@ SIGNATURES = {
     "gg_read_status": (_int, [_vp, _vp, _vp]),
     "gg_set_gemm_schedule": (_int, [_int]),
     "gg_selftest_bounded_wait": (_int, [_vp, _vp, ctypes.c_uint64, _vp]),
+    "gg_selftest_block_norm_wait": (_int, [_vp, _vp, _int, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
     "gg_selftest_block_norm_bwd_wait": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
     "gg_route_workspace_size": (_sz, [_i64, _int, _int]),
     "gg_route_hist_offsets": (_int, [_vp, _i64, _int, _int, _int, _vp, _vp, _vp, _vp, _vp, _vp, _sz,

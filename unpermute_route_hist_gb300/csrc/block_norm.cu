@@ -28,6 +28,7 @@ struct NormFwd {
     int32_t* status;
     int stages, stage_bytes, slots, groups;  // expert rows a stage, stages a token
     int st32;                                // output rows start 32-byte aligned
+    Probe probe;
 };
 
 enum Keep { KEEP_NONE = 0, KEEP_BF16 = 1, KEEP_INT8 = 2, KEEP_E4M3 = 3 };
@@ -81,7 +82,7 @@ __device__ __forceinline__ void keep_unit(const Cols<F32, FULL>& cols, const Uni
 // Sums of up to three rows take 80 registers, so that three CTAs of 256 threads share an SM
 // (8192 x 4096 with two rows a token: 69 us with two CTAs, 59 with three; eight rows of 2048
 // columns: 138 and 150); the others two.  SPLIT: a cluster's two CTAs have halves of each row.
-template <bool F32, int KEEP, bool SPLIT, bool FULL, int SRC>
+template <bool F32, int KEEP, bool SPLIT, bool FULL, int SRC, bool PROBE = false>
 __global__ void __maxnreg__(SRC == SRC_FEW ? 80 : 128) block_norm_kernel(const NormFwd p) {
     constexpr bool SUM = SRC >= SRC_FEW;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -117,6 +118,9 @@ __global__ void __maxnreg__(SRC == SRC_FEW ? 80 : 128) block_norm_kernel(const N
     // weight of an expert row are read one stage before they are needed.
     int64_t t_in = first;
     int g_in = 0, s_in = 0;
+    auto issued = [&]() { return (t_in - first) / step * groups + g_in; };
+    Account<PROBE> account;
+    constexpr uint64_t limit = PROBE ? kProbeWaitNs : kWaitLimitNs;
     int32_t row_in = -1;
     float w_in = 1.f;
     auto look_up = [&]() {
@@ -132,7 +136,9 @@ __global__ void __maxnreg__(SRC == SRC_FEW ? 80 : 128) block_norm_kernel(const N
         if (t_in >= p.T) return;
         uint8_t* stage = ring + s_in * p.stage_bytes;
         uint64_t* bar = &ctl->full[s_in];
+        if constexpr (PROBE) account.fill(ctl, p.stages, issued());
         if constexpr (SUM) {
+            const bool held = PROBE && t_in == p.probe.withheld && g_in == 0 && side == 0;
             const bool slot = lane < p.slots && g_in * p.slots + lane < p.topk;
             const bool ok = slot && row_in >= 0 && row_in < p.T * p.topk;
             if (slot) {
@@ -141,7 +147,7 @@ __global__ void __maxnreg__(SRC == SRC_FEW ? 80 : 128) block_norm_kernel(const N
             }
             const uint32_t hb = lane == 0 && g_in == groups - 1 ? K * hs : 0;
             mbar_arrive_expect_tx(bar, (ok ? row_bytes : 0) + hb);
-            if (ok) bulk_row(stage + lane * row_area, from_y + static_cast<int64_t>(row_in) * p.K, row_bytes, bar);
+            if (ok && !held) bulk_row(stage + lane * row_area, from_y + static_cast<int64_t>(row_in) * p.K, row_bytes, bar);
             if (hb) bulk_row(stage + h_at, from_h + t_in * (p.K * hs), hb, bar);
             if (++g_in == groups) {
                 g_in = 0;
@@ -173,6 +179,7 @@ __global__ void __maxnreg__(SRC == SRC_FEW ? 80 : 128) block_norm_kernel(const N
     const int code_pitch = static_cast<int>(act8_code_pitch(p.K)), scale_pitch = static_cast<int>(act8_scale_pitch(p.K));
     int stage = 0;
     uint32_t parity = 0, calls = 0;
+    bool left = false;
     for (int64_t t = first; t < p.T; t += ROWS * step) {
         const int rows = ROWS == 1 || t + step < p.T ? ROWS : 1;
         float tg[ROWS];
@@ -192,7 +199,8 @@ __global__ void __maxnreg__(SRC == SRC_FEW ? 80 : 128) block_norm_kernel(const N
             }
             for (int g = 0; g < groups; ++g) {
                 const uint8_t* at = ring + stage * p.stage_bytes;
-                wait_row(&ctl->full[stage], parity, ctl, p.status);
+                wait_row(&ctl->full[stage], parity, ctl, p.status, limit);
+                account.waited();
                 if constexpr (SUM) {
                     const int n = min(p.slots, p.topk - g * p.slots);
                     for (int j = 0; j < n; ++j) {
@@ -221,12 +229,11 @@ __global__ void __maxnreg__(SRC == SRC_FEW ? 80 : 128) block_norm_kernel(const N
                 // a stage that the next row or group needs before the row sums' barrier
                 if (!last || (ROWS == 2 && r == 0 && p.stages == 1)) {
                     __syncthreads();
-                    refill();
+                    if (!given_up(ctl)) refill();
                 }
             }
         }
         float q[ROWS];
-        bool left;
         if (SPLIT || (SRC != SRC_NONE && p.w_post)) {
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
@@ -244,10 +251,7 @@ __global__ void __maxnreg__(SRC == SRC_FEW ? 80 : 128) block_norm_kernel(const N
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) q[r] = 1.f;
         }
-        if (left) {
-            if (threadIdx.x == 0) drain_ring(ctl, p.stages, (t_in - first) / step * groups + g_in);
-            break;
-        }
+        if (left) break;
         // every thread holds the rows in registers
         refill();
         if (ROWS == 2 && rows == 2 && p.stages > 1) refill();
@@ -280,7 +284,8 @@ __global__ void __maxnreg__(SRC == SRC_FEW ? 80 : 128) block_norm_kernel(const N
             for (int k = 0; k < 8; ++k) s2 = fma2(h[r].v[k], h[r].v[k], s2);
             n[r] = both(s2);
         }
-        (void)row_sum<ROWS, SPLIT>(n, ctl, calls, p.status);
+        left = row_sum<ROWS, SPLIT>(n, ctl, calls, p.status);
+        if (left) break;
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             if (r >= rows) continue;
@@ -293,6 +298,11 @@ __global__ void __maxnreg__(SRC == SRC_FEW ? 80 : 128) block_norm_kernel(const N
             cols.put_bf16(to_x, p.st32, h[r]);
         }
     }
+    if (left && threadIdx.x == 0) {
+        drain_ring(ctl, p.stages, issued(), limit);
+        account.drained();
+    }
+    account.put(p.probe, left, issued());
     if (SPLIT) leave_pair();
 }
 
@@ -330,15 +340,17 @@ int launch_fwd(int keep, const NormFwd& p, const Launch& l) {
     if (p.topk <= kFewRows && !l.split) return launch_fwd<F32, SRC_FEW>(keep, p, l);
     return launch_fwd<F32, SRC_SLOTS>(keep, p, l);
 }
-}  // namespace
-}  // namespace gg
+// The diagnostic form: sums of more rows, a bf16 stream.
+int launch_probe(const NormFwd& p, const Launch& l) {
+    static std::atomic<uint64_t> done[2];
+    return l.split ? launch(block_norm_kernel<false, KEEP_NONE, true, false, SRC_SLOTS, true>, done[0], p, true, l.rows, l.threads, l.smem, l.st)
+                   : launch(block_norm_kernel<false, KEEP_NONE, false, false, SRC_SLOTS, true>, done[1], p, false, l.rows, l.threads, l.smem, l.st);
+}
 
-using namespace gg;
-
-extern "C" int gg_block_norm(const void* h, int h_dtype, const gg_bf16* Y, const int32_t* row_id_map, const float* topk_w,
-                  int topk, const float* w_post, const float* gate, const float* token_gate, float res_scale,
-                  const float* w_pre, float eps, int64_t T, int64_t K, void* out_h, gg_bf16* out_x, gg_bf16* out_y,
-                  uint8_t* y_codes, uint8_t* y_scales, int fmt, int32_t* status, void* stream) {
+int block_norm(const void* h, int h_dtype, const gg_bf16* Y, const int32_t* row_id_map, const float* topk_w, int topk,
+               const float* w_post, const float* gate, const float* token_gate, float res_scale, const float* w_pre,
+               float eps, int64_t T, int64_t K, void* out_h, gg_bf16* out_x, gg_bf16* out_y, uint8_t* y_codes,
+               uint8_t* y_scales, int fmt, int32_t* status, void* stream, const Probe* probe) {
     if (T < 0 || K < 0 || topk < 1) return GG_ERR_INVALID_ARG;
     if (h_dtype != GG_DTYPE_BF16 && h_dtype != GG_DTYPE_F32) return GG_ERR_INVALID_ARG;
     if (fmt != GG_ACT8_INT8 && fmt != GG_ACT8_E4M3) return GG_ERR_INVALID_ARG;
@@ -393,6 +405,38 @@ extern "C" int gg_block_norm(const void* h, int h_dtype, const gg_bf16* Y, const
     const int threads = norm_threads(K);
     const Launch l{norm_split(K), p.st32 && K == 16 * threads, static_cast<unsigned>(T < most ? T : most), threads,
                    sizeof(Ctl) + static_cast<size_t>(p.stages) * p.stage_bytes, static_cast<cudaStream_t>(stream)};
+    if (probe) {
+        p.probe = *probe;
+        return launch_probe(p, l);
+    }
     const int keep = out_y ? KEEP_BF16 : !y_codes ? KEEP_NONE : fmt == GG_ACT8_INT8 ? KEEP_INT8 : KEEP_E4M3;
     return f32 ? launch_fwd<true>(keep, p, l) : launch_fwd<false>(keep, p, l);
 }
+
+}  // namespace
+}  // namespace gg
+
+using namespace gg;
+
+extern "C" {
+
+int gg_block_norm(const void* h, int h_dtype, const gg_bf16* Y, const int32_t* row_id_map, const float* topk_w,
+                  int topk, const float* w_post, const float* gate, const float* token_gate, float res_scale,
+                  const float* w_pre, float eps, int64_t T, int64_t K, void* out_h, gg_bf16* out_x, gg_bf16* out_y,
+                  uint8_t* y_codes, uint8_t* y_scales, int fmt, int32_t* status, void* stream) {
+    return block_norm(h, h_dtype, Y, row_id_map, topk_w, topk, w_post, gate, token_gate, res_scale, w_pre, eps, T, K, out_h,
+                      out_x, out_y, y_codes, y_scales, fmt, status, stream, nullptr);
+}
+
+int gg_selftest_block_norm_wait(const gg_bf16* h, const gg_bf16* Y, int topk, const float* w, int64_t T, int64_t K,
+                                int64_t withheld, gg_bf16* out_h, gg_bf16* out_x, int32_t* record, int32_t* status,
+                                void* stream) {
+    if (!Y || !w || !record || !status || withheld < 0 || withheld >= T || topk <= kFewRows) return GG_ERR_INVALID_ARG;
+    Probe probe;
+    probe.withheld = withheld;
+    probe.record = record;
+    return block_norm(h, GG_DTYPE_BF16, Y, nullptr, nullptr, topk, w, nullptr, nullptr, 1.f, w, 1e-6f, T, K, out_h, out_x,
+                      nullptr, nullptr, nullptr, GG_ACT8_INT8, status, stream, &probe);
+}
+
+}  // extern "C"
