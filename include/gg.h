@@ -593,6 +593,9 @@ int gg_block_norm(const void* h, int h_dtype, const gg_bf16* Y, const int32_t* r
  *  Outputs, the workspace among them, overlap neither inputs nor one another
  *  (GG_ERR_INVALID_ARG), but out_dh may be dh: the whole of it, and then no other input's
  *  memory, but for dx, h or y of the same address and as long rows.
+ *  A row whose squares' sum passes fp32's range (which the forward norms to zeros) gets the
+ *  zero gradient through that norm; where products of its elements with the gradients pass
+ *  it too, NaN, and so do the vectors'.
  *  Deterministic (fixed summation orders). */
 size_t gg_block_norm_bwd_workspace_size(int64_t T, int64_t K);
 int gg_block_norm_bwd(const void* dh, const gg_bf16* dx, const void* h, int h_dtype,
