@@ -193,7 +193,9 @@ act8_pack_kernel(const void* __restrict__ X, int64_t rows, int C, FastDiv vecs, 
 // by HBM: 8192 x 4096 as it is 17 us, each row twice in another order 29 us, 16384 x 2048 each
 // row eight times 91 us (the copy rate: 15, 25, 84; 4.7 us are a launch's own).  Outputs leave
 // L2 first and gathered codes last, or the outputs push out rows that are read again (34 and
-// 122 us); gathered rows want four pieces' loads in flight (30 and 97 us with two).
+// 122 us); gathered rows want four pieces' loads in flight (30 and 97 us with two).  What runs
+// behind takes as long as with codes that leave like any line (dW of 8192 x 4096 twice 2.29 and
+// 2.28 ms within a span of 2.13-2.32, of 16384 x 2048 eight times 657-672 and 671-682 us).
 template <int DT, int FMT, int W>
 __global__ void __launch_bounds__(kThreads)
 act8_unpack_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t src_rows, int C,

@@ -28,7 +28,7 @@ constexpr int kMaxThreads = 512;
 constexpr int kMaxStages = 8;
 constexpr int kMaxSlots = 32;           // expert rows of a stage, one lane each
 constexpr int kSmemBudget = 228 * 1024;  // an SM's shared memory, for all its CTAs
-constexpr int kGridSms = 152;
+constexpr int kGridSms = 152;  // (a constant: the workspace's size is asked for without a device)
 
 struct Slot {
     float w;
