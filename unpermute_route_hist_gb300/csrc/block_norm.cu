@@ -435,6 +435,7 @@ int gg_selftest_block_norm_wait(const gg_bf16* h, const gg_bf16* Y, int topk, co
                                 int64_t withheld, gg_bf16* out_h, gg_bf16* out_x, int32_t* record, int32_t* status,
                                 void* stream) {
     if (!Y || !w || !record || !status || withheld < 0 || withheld >= T || topk <= kFewRows) return GG_ERR_INVALID_ARG;
+    if (!aligned(record, 4) || !aligned(status, 4)) return GG_ERR_UNSUPPORTED;
     Probe probe;
     probe.withheld = withheld;
     probe.record = record;

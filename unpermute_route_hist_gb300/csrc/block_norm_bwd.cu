@@ -496,6 +496,7 @@ int gg_selftest_block_norm_bwd_wait(const gg_bf16* dx, const gg_bf16* h, const g
                                     int64_t K, int64_t withheld, gg_bf16* out_dh, gg_bf16* dy, int32_t* record,
                                     int32_t* status, void* stream) {
     if (!dx || !y || !w || !out_dh || !dy || !record || !status || withheld < 0 || withheld >= T) return GG_ERR_INVALID_ARG;
+    if (!aligned(record, 4) || !aligned(status, 4)) return GG_ERR_UNSUPPORTED;
     Probe probe;
     probe.withheld = withheld;
     probe.record = record;
